@@ -195,11 +195,14 @@ def _on_list(s, rows=slice(None)):
 
 
 def _stats(s):
-    """Per row: log sum exp(s / T), and the log of the student's mass off the list."""
-    z = s["logits"].float() / s["temperature"]
+    """Per row: the largest logit m, log sum exp((s - m) / T), and the log of
+    the student's mass off the list."""
+    z = s["logits"].float()
+    top = z.amax(1, keepdim=True)
+    z = (z - top) / s["temperature"]
     lse = torch.logsumexp(z, 1)
     off = torch.logsumexp(z.masked_fill_(_on_list(s), float("-inf")), 1) - lse
-    return torch.stack([lse, off], 1)
+    return torch.stack([top[:, 0], lse, off], 1)
 
 
 def prepare(case, seed):
@@ -261,8 +264,8 @@ def _plain_distill(s):
     temp, w = s["temperature"], s["weight"]
     on = _on_list(s) if rest is not None else None
     if s["what"] == "grad":
-        log_q = z / temp - s["stats"][:, :1]
-        log_off = s["stats"][:, 1]
+        log_q = (z - s["stats"][:, :1]) / temp - s["stats"][:, 1:2]
+        log_off = s["stats"][:, 2]
     else:
         # the largest logit goes off before the division: what the
         # exponential sees is then exact to its own size
