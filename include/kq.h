@@ -76,7 +76,9 @@ typedef enum {
   KQ_OP_LAYER_OBJECTIVE = 6,
   KQ_OP_APPLY_QUANTIZED = 7, /* n_tok argument of kq_workspace_size = batch */
   KQ_OP_YAQA_QUANTIZE = 8,
-  KQ_OP_APPLY_QUANTIZED_A4 = 9 /* n_tok argument of kq_workspace_size = batch */
+  KQ_OP_APPLY_QUANTIZED_A4 = 9, /* n_tok argument of kq_workspace_size = batch */
+  KQ_OP_MATMUL_I8 = 10,
+  KQ_OP_LINEAR_I8 = 11
 } kq_op;
 
 /* Grid and sweep configuration (KronQ summary, Method and experiments:
@@ -144,7 +146,8 @@ kq_status kq_set_kernel_events(kq_op op, hipEvent_t start, hipEvent_t stop);
 kq_status kq_set_gemm_tile(int tile);
 
 /* Bytes of scratch memory `op` needs for the given sizes (host output).
- * n_tok and dtype matter for KQ_OP_ACCUMULATE_COV only; cfg for
+ * n_tok matters for KQ_OP_ACCUMULATE_COV, the inference ops and the 8-bit
+ * products (where it may be 0), dtype for KQ_OP_ACCUMULATE_COV only; cfg for
  * KQ_OP_GPTAQ_QUANTIZE only (may be NULL elsewhere). For square-matrix ops
  * (CHOLESKY_INV, FORM_P) pass the matrix order as d_in. */
 kq_status kq_workspace_size(kq_op op, int64_t d_out, int64_t d_in, int64_t n_tok,
@@ -380,6 +383,122 @@ kq_status kq_apply_quantized_a4(const uint32_t* packed, const float* scale, cons
                                 const float* x, int64_t batch, int64_t d_out, int64_t d_in,
                                 float clip, float* y, int8_t* act_codes, float* act_scale,
                                 void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Product in 8-bit integers with a scale for each token and each channel
+ * (the weight-and-activation setting of KronQ explainer, gist.science,
+ * "Quantizzazione di Pesi e Attivazioni", at 8 bits):
+ *   s_t  = clip * max_k |x_tk| / 127
+ *   a_tk = clamp(rint(x_tk / s_t), -127, 127)            (fp32, ties to even)
+ *   y_to = s_t w_o (sum_k a_tk (q_ok - z_o)) + b_o
+ * The sum is exact (int32); the scales and the bias are applied in fp32 and
+ * y is rounded once. The layer is used in the basis its codes were made in:
+ * no Hadamard transform is applied.
+ *
+ * Code rows, of tokens and of channels, are int8 and padded with zeros to
+ * kq_i8_row_bytes(d_in) bytes (a multiple of 128); code buffers are 16-byte
+ * aligned. Matrices of these calls have a row stride of their own, in
+ * elements (ldx >= d_in, ldy >= d_out), and need only the alignment of their
+ * element type. KQ_BF16 or KQ_F32 for x and y, independently. n_tok may be 0:
+ * nothing is launched, and the pointers are not looked at. 1 <= d_in <= 65536;
+ * n_tok, d_out <= 1048576. Asynchronous. */
+
+/* Bytes of one padded row of codes (host output). */
+kq_status kq_i8_row_bytes(int64_t d_in, int64_t* bytes);
+
+/* Rows of x (n x d_in) onto symmetric 8-bit grids of their own: tokens, or
+ * the channels of a weight matrix to be rounded to nearest.
+ *   codes  n rows of kq_i8_row_bytes(d_in) bytes;  scale  n floats;
+ *   sums   n int32: the sum of each row's codes
+ * A row of zeros (or one whose scale underflows to 0) has scale 0 and codes
+ * 0. A row that holds a NaN or an infinity has scale NaN and codes 0, so
+ * that its products are NaN. 0 < clip <= 1. */
+kq_status kq_quantize_rows(const void* x, kq_dtype dt, int64_t n, int64_t d_in, int64_t ldx,
+                           float clip, int8_t* codes, float* scale, int32_t* sums,
+                           hipStream_t stream);
+
+/* Codes of the sweep (d_out x d_in uint8, any width up to 8 bits, one grid per
+ * channel) as rows of signed codes q - 128, and their zeros as zero - 128.
+ * zero, zero_out: d_out floats (integers in [0, 255] and [-128, 127]). */
+kq_status kq_pack_i8(const uint8_t* codes, const float* zero, int64_t d_out, int64_t d_in,
+                     int8_t* packed, float* zero_out, hipStream_t stream);
+
+/* y from tokens that are quantized already (several layers may share them).
+ *   a, a_scale, a_sum  kq_quantize_rows of the tokens (a_sum may be NULL if
+ *                      w_zero is)
+ *   w, w_scale         d_out rows of codes and their scales
+ *   w_zero             d_out floats, integers in [-128, 127]; NULL: zeros
+ *   bias               d_out floats; NULL: none
+ * Workspace from kq_workspace_size(KQ_OP_MATMUL_I8, d_out, d_in, n_tok). */
+kq_status kq_matmul_i8(const int8_t* a, const float* a_scale, const int32_t* a_sum,
+                       const int8_t* w, const float* w_scale, const float* w_zero,
+                       const float* bias, int64_t n_tok, int64_t d_out, int64_t d_in, void* y,
+                       kq_dtype dt, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* kq_quantize_rows of x (n_tok x d_in) and kq_matmul_i8 in one call.
+ * Workspace from kq_workspace_size(KQ_OP_LINEAR_I8, d_out, d_in, n_tok). */
+kq_status kq_linear_i8(const void* x, kq_dtype dt, int64_t ldx, float clip, const int8_t* w,
+                       const float* w_scale, const float* w_zero, const float* bias,
+                       int64_t n_tok, int64_t d_out, int64_t d_in, void* y, kq_dtype y_dt,
+                       int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Distillation from a teacher's top logits (notes on YAQA, arXiv 2505.22988:
+ * the KL divergence to the original model's answers is what quantization is
+ * to keep small; its gradient is the G of kq_accumulate_cov).
+ *
+ * Logits are n x vocab, KQ_BF16 or KQ_F32, with row stride ld >= vocab (in
+ * elements) and the alignment of their element type. n may be 0: nothing is
+ * launched, and the pointers are not looked at. n <= 1048576, 1 <= k <= 256,
+ * temperature T finite and > 0. Asynchronous, no workspace. */
+
+/* The k largest logits of each row in descending order (equal ones by lowest
+ * index; a NaN counts as larger than any number, +0 and -0 as equal):
+ *   values  n x k floats;  index  n x k int32
+ *   lse     n floats: log sum_j exp(logits_j / T) over the whole row, or NULL
+ * k <= vocab <= 2^31 - 1. */
+kq_status kq_top_logits(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld,
+                        int32_t k, float temperature, float* values, int32_t* index, float* lse,
+                        hipStream_t stream);
+
+/* With q = softmax(s / T) of the student's logits s and the teacher's list
+ * (t_values, t_index: n x k, the logits and columns of kq_top_logits):
+ *   t_lse NULL:  p = softmax of the list's t / T;  r = 0
+ *   t_lse given: p_k = exp(t_k / T - t_lse);  r = 1 - sum_k p_k is the
+ *                teacher's mass off the list, against the student's q_r = sum
+ *                of q off the list (r <= 2^-16 counts as 0: t_lse is fp32)
+ *   loss    = w T^2 [ sum_k p_k (log p_k - log q_k) + r (log r - log q_r) ]
+ *   dloss/ds_j = w T [ c_j q_j - p_j ],  c_j = P on the list and P - r / q_r
+ *                off it, P = sum_k p_k + r
+ *   weight  n floats w (a row of weight 0 gets loss and gradient 0, and its
+ *           logits are not looked at), or NULL for ones
+ *   loss    n floats
+ *   stats   n x 3 floats for kq_distill_grad: the largest logit m,
+ *           log sum exp((s - m) / T), log q_r; or NULL
+ * An entry whose index is below 0 or at least vocab is none (lists may have
+ * fewer than k entries, or none); entries of the same index add up. A row
+ * whose logits are all -inf has q = 0. vocab <= 524288. */
+kq_status kq_distill_loss(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld,
+                          const float* t_values, const int32_t* t_index, const float* t_lse,
+                          int32_t k, float temperature, const float* weight, float* loss,
+                          float* stats, hipStream_t stream);
+
+/* The gradient from the stats of the forward call and the gradient of each
+ * row's loss (dloss, n floats, in place of w above).
+ *   grad    n x vocab of the logits' type with row stride ldg >= vocab; it
+ *           may be the logits themselves (ldg = ld). */
+kq_status kq_distill_grad(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld,
+                          const float* t_values, const int32_t* t_index, const float* t_lse,
+                          int32_t k, float temperature, const float* stats, const float* dloss,
+                          void* grad, int64_t ldg, hipStream_t stream);
+
+/* Loss and gradient in one call (the gradient of sum_rows loss; weight as
+ * above; stats may be NULL). */
+kq_status kq_distill_loss_grad(const void* logits, kq_dtype dt, int64_t n, int64_t vocab,
+                               int64_t ld, const float* t_values, const int32_t* t_index,
+                               const float* t_lse, int32_t k, float temperature,
+                               const float* weight, float* loss, float* stats, void* grad,
+                               int64_t ldg, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -18,6 +18,7 @@ against closed forms, brute force or library routines. One result is
 full-size workloads, since the pages print no worked example.
 """
 from . import deploy  # noqa: F401
+from . import head  # noqa: F401
 from . import yaqa  # noqa: F401
 from .kronq import (  # noqa: F401
     allocate_bits,

@@ -18,14 +18,23 @@ from .api import (  # noqa: F401
     kq_apply_quantized_noalloc,
     kq_biip,
     kq_cholesky_inv,
+    kq_distill_grad,
+    kq_distill_loss,
+    kq_distill_loss_grad,
     kq_form_p,
     kq_gptaq_quantize,
+    kq_i8_row_bytes,
+    kq_linear_i8,
+    kq_matmul_i8,
     kq_yaqa_quantize,
     kq_layer_objective,
     kq_pack_codes,
+    kq_pack_i8,
     kq_packed_row_words,
+    kq_quantize_rows,
     kq_sensitivity,
     kq_set_kernel_events,
     kq_set_gemm_tile,
+    kq_top_logits,
     kq_workspace_size,
 )

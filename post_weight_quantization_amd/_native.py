@@ -19,14 +19,16 @@ KQ_BF16, KQ_F32 = 0, 1
 KQ_NOALLOC_SCRATCH_BYTES = 64 << 20  # include/kq.h
 (KQ_OP_ACCUMULATE_COV, KQ_OP_BIIP, KQ_OP_SENSITIVITY, KQ_OP_CHOLESKY_INV, KQ_OP_FORM_P,
  KQ_OP_GPTAQ_QUANTIZE, KQ_OP_LAYER_OBJECTIVE, KQ_OP_APPLY_QUANTIZED,
- KQ_OP_YAQA_QUANTIZE, KQ_OP_APPLY_QUANTIZED_A4) = range(10)
+ KQ_OP_YAQA_QUANTIZE, KQ_OP_APPLY_QUANTIZED_A4, KQ_OP_MATMUL_I8, KQ_OP_LINEAR_I8) = range(12)
 
 # every symbol include/kq.h declares
 EXPORTS = ("kq_last_error", "kq_version", "kq_workspace_size", "kq_accumulate_cov", "kq_biip",
            "kq_sensitivity", "kq_cholesky_inv", "kq_form_p", "kq_gptaq_quantize",
            "kq_allocate_bits", "kq_layer_objective", "kq_set_kernel_events",
            "kq_packed_row_words", "kq_pack_codes", "kq_apply_quantized", "kq_yaqa_quantize",
-           "kq_apply_quantized_a4", "kq_apply_quantized_noalloc", "kq_set_gemm_tile")
+           "kq_apply_quantized_a4", "kq_apply_quantized_noalloc", "kq_set_gemm_tile",
+           "kq_i8_row_bytes", "kq_quantize_rows", "kq_pack_i8", "kq_matmul_i8", "kq_linear_i8",
+           "kq_top_logits", "kq_distill_loss", "kq_distill_grad", "kq_distill_loss_grad")
 
 
 class kq_quant_cfg(ctypes.Structure):
@@ -91,6 +93,18 @@ _sig("kq_apply_quantized_noalloc", _st, _p, ctypes.c_int32, _p, _p, ctypes.c_int
      _i64, _p, _i64, _i64, _i64, _p, _p)
 _sig("kq_apply_quantized_a4", _st, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _p, _i64, _i64, _i64,
      ctypes.c_float, _p, _p, _p, _p, _sz, _p)
+_i32, _f = ctypes.c_int32, ctypes.c_float
+_sig("kq_i8_row_bytes", _st, _i64, _p)
+_sig("kq_quantize_rows", _st, _p, ctypes.c_int, _i64, _i64, _i64, _f, _p, _p, _p, _p)
+_sig("kq_pack_i8", _st, _p, _p, _i64, _i64, _p, _p, _p)
+_sig("kq_matmul_i8", _st, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p, ctypes.c_int, _i64, _p, _sz, _p)
+_sig("kq_linear_i8", _st, _p, ctypes.c_int, _i64, _f, _p, _p, _p, _p, _i64, _i64, _i64, _p, ctypes.c_int,
+     _i64, _p, _sz, _p)
+_sig("kq_top_logits", _st, _p, ctypes.c_int, _i64, _i64, _i64, _i32, _f, _p, _p, _p, _p)
+_sig("kq_distill_loss", _st, _p, ctypes.c_int, _i64, _i64, _i64, _p, _p, _p, _i32, _f, _p, _p, _p, _p)
+_sig("kq_distill_grad", _st, _p, ctypes.c_int, _i64, _i64, _i64, _p, _p, _p, _i32, _f, _p, _p, _p, _i64, _p)
+_sig("kq_distill_loss_grad", _st, _p, ctypes.c_int, _i64, _i64, _i64, _p, _p, _p, _i32, _f, _p, _p, _p, _p,
+     _i64, _p)
 
 
 def check(status: int, info: int = 0) -> None:

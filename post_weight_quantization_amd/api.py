@@ -395,3 +395,241 @@ def kq_apply_quantized_a4(packed, scale, zero, s_x, s_g, sign_in, sign_out, x, c
                                       d_out, d_in, float(clip), _ptr(y), _ptr(act_codes),
                                       _ptr(act_scale), _ptr(ws), _nbytes(ws), _stream(stream)))
     return y
+
+
+# ------------------------------------------------- 8-bit product, distillation
+_DT = {torch.bfloat16: N.KQ_BF16, torch.float32: N.KQ_F32}
+
+
+def _raw_stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor in the memory of the stream that the call runs on: no
+    earlier work of another stream can still be using that memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, name, cols=None, dtypes=(torch.bfloat16, torch.float32)):
+    """(rows, columns, row stride in elements) of a 2-D matrix whose rows may
+    lie further apart than they are long."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in dtypes or (
+            cols is not None and t.shape[1] != cols):
+        want = " or ".join(str(d) for d in dtypes)
+        got = f"{tuple(t.shape)} {t.dtype}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name}: expected a matrix of {want}" +
+                         (f" with {cols} columns" if cols is not None else "") + f", got {got}")
+    n, m = t.shape
+    if m < 1:
+        raise ValueError(f"{name}: expected at least one column")
+    if m > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: expected rows of adjacent elements, got strides {t.stride()}")
+    ld = t.stride(0) if n > 1 else m
+    if ld < m:
+        raise ValueError(f"{name}: expected rows that do not overlap, got strides {t.stride()}")
+    return n, m, ld
+
+
+def _flat(t, count, dtype, name):
+    """A contiguous tensor of `count` elements, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.numel() != count or not t.is_contiguous():
+        got = f"{tuple(t.shape)} {t.dtype}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name}: expected {count} contiguous {dtype}, got {got}")
+    return t.data_ptr()
+
+
+def _on_device(device, *ts):
+    if device.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors must be on one GPU, got {device} and {t.device}")
+
+
+def kq_i8_row_bytes(d_in: int) -> int:
+    """Bytes of one row of 8-bit codes (d_in padded to a multiple of 128)."""
+    out = ctypes.c_int64(0)
+    check(N.lib.kq_i8_row_bytes(d_in, ctypes.byref(out)))
+    return out.value
+
+
+def _codes(t, rows, d_in, name):
+    rb = kq_i8_row_bytes(d_in)
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int8 or tuple(t.shape) != (rows, rb) or \
+            not t.is_contiguous():
+        got = f"{tuple(t.shape)} {t.dtype}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name}: expected contiguous int8 codes {(rows, rb)}, got {got}")
+    return t.data_ptr()
+
+
+def kq_quantize_rows(x, clip: float = 1.0, codes=None, scale=None, sums=None, stream=None):
+    """Rows of x (n x d_in, bf16 or fp32) onto symmetric 8-bit grids of their
+    own; returns (codes int8 n x row bytes, scale fp32 n, sums int32 n)."""
+    n, d, ldx = _rows(x, "x")
+    dev = x.device
+    _on_device(dev, codes, scale, sums)
+    if codes is None:
+        codes = _empty((n, kq_i8_row_bytes(d)), torch.int8, dev, stream)
+    if scale is None:
+        scale = _empty((n,), torch.float32, dev, stream)
+    if sums is None:
+        sums = _empty((n,), torch.int32, dev, stream)
+    check(N.lib.kq_quantize_rows(x.data_ptr(), _DT[x.dtype], n, d, ldx, clip, _codes(codes, n, d, "codes"),
+                                 _flat(scale, n, torch.float32, "scale"), _flat(sums, n, torch.int32, "sums"),
+                                 _raw_stream(stream, dev)))
+    return codes, scale, sums
+
+
+def kq_pack_i8(codes, zero, packed=None, zero_out=None, stream=None):
+    """The sweep's codes (d_out x d_in uint8) and zeros (one per channel) as
+    (signed codes int8 d_out x row bytes, zeros fp32 d_out) of the 8-bit product."""
+    d_out, d_in = codes.shape
+    dev = codes.device
+    pc = _flat(codes, d_out * d_in, torch.uint8, "codes")
+    pz = _flat(zero, d_out, torch.float32, "zero")
+    if pz is None:
+        raise ValueError("zero: expected a tensor")
+    _on_device(dev, zero, packed, zero_out)
+    if packed is None:
+        packed = _empty((d_out, kq_i8_row_bytes(d_in)), torch.int8, dev, stream)
+    if zero_out is None:
+        zero_out = _empty((d_out,), torch.float32, dev, stream)
+    check(N.lib.kq_pack_i8(pc, pz, d_out, d_in, _codes(packed, d_out, d_in, "packed"),
+                           _flat(zero_out, d_out, torch.float32, "zero_out"), _raw_stream(stream, dev)))
+    return packed, zero_out
+
+
+def _product_out(y, n, d_out, dtype, dev, stream):
+    if y is None:
+        y = _empty((n, d_out), dtype, dev, stream)
+        return y, d_out
+    rows, _, ldy = _rows(y, "y", d_out)
+    if rows != n:
+        raise ValueError(f"y: expected {n} rows, got {rows}")
+    return y, ldy
+
+
+def kq_matmul_i8(a, a_scale, w, w_scale, d_in: int, a_sum=None, w_zero=None, bias=None, y=None,
+                 dtype=torch.bfloat16, ws=None, stream=None):
+    """y (n x d_out) = s_t w_o (sum_k a_tk (q_ok - z_o)) + b_o from tokens
+    already quantized by kq_quantize_rows. dtype: of y where y is not given."""
+    n, d_out = a.shape[0], w.shape[0]
+    dev = a.device
+    _on_device(dev, a_scale, w, w_scale, a_sum, w_zero, bias, y, ws)
+    pa, pw = _codes(a, n, d_in, "a"), _codes(w, d_out, d_in, "w")
+    f32 = torch.float32
+    y, ldy = _product_out(y, n, d_out, dtype, dev, stream)
+    if ws is None:
+        need = kq_workspace_size(N.KQ_OP_MATMUL_I8, d_out, d_in, n)
+        ws = _empty((need,), torch.uint8, dev, stream) if need else None
+    check(N.lib.kq_matmul_i8(pa, _flat(a_scale, n, f32, "a_scale"), _flat(a_sum, n, torch.int32, "a_sum"), pw,
+                             _flat(w_scale, d_out, f32, "w_scale"), _flat(w_zero, d_out, f32, "w_zero"),
+                             _flat(bias, d_out, f32, "bias"), n, d_out, d_in, y.data_ptr(), _DT[y.dtype], ldy,
+                             None if ws is None else ws.data_ptr(), 0 if ws is None else _nbytes(ws),
+                             _raw_stream(stream, dev)))
+    return y
+
+
+def kq_linear_i8(x, w, w_scale, w_zero=None, bias=None, clip: float = 1.0, y=None, dtype=None, ws=None,
+                 stream=None):
+    """y (n x d_out) of the 8-bit layer for tokens x (n x d_in, bf16 or fp32):
+    kq_quantize_rows and kq_matmul_i8 in one call. dtype: of y where y is not
+    given (default: that of x)."""
+    n, d_in, ldx = _rows(x, "x")
+    d_out = w.shape[0]
+    dev = x.device
+    _on_device(dev, w, w_scale, w_zero, bias, y, ws)
+    pw = _codes(w, d_out, d_in, "w")
+    f32 = torch.float32
+    y, ldy = _product_out(y, n, d_out, dtype or x.dtype, dev, stream)
+    if ws is None:
+        ws = _empty((kq_workspace_size(N.KQ_OP_LINEAR_I8, d_out, d_in, n),), torch.uint8, dev, stream)
+    check(N.lib.kq_linear_i8(x.data_ptr(), _DT[x.dtype], ldx, clip, pw, _flat(w_scale, d_out, f32, "w_scale"),
+                             _flat(w_zero, d_out, f32, "w_zero"), _flat(bias, d_out, f32, "bias"), n, d_out,
+                             d_in, y.data_ptr(), _DT[y.dtype], ldy, ws.data_ptr(), _nbytes(ws),
+                             _raw_stream(stream, dev)))
+    return y
+
+
+def kq_top_logits(logits, k: int, temperature: float = 1.0, want_lse: bool = True, stream=None):
+    """The k largest logits of each row (n x vocab, bf16 or fp32): (values
+    fp32 n x k in descending order, index int32 n x k, lse fp32 n of
+    logits / temperature, None without want_lse)."""
+    n, vocab, ld = _rows(logits, "logits")
+    dev = logits.device
+    _on_device(dev)
+    values = _empty((n, k), torch.float32, dev, stream)
+    index = _empty((n, k), torch.int32, dev, stream)
+    lse = _empty((n,), torch.float32, dev, stream) if want_lse else None
+    check(N.lib.kq_top_logits(logits.data_ptr(), _DT[logits.dtype], n, vocab, ld, k, temperature,
+                              values.data_ptr(), index.data_ptr(), lse.data_ptr() if want_lse else None,
+                              _raw_stream(stream, dev)))
+    return values, index, lse
+
+
+def _distill_args(logits, values, index, t_lse, temperature, rows, name, *others):
+    """The leading arguments that the three distillation calls share."""
+    n, vocab, ld = _rows(logits, "logits")
+    if not isinstance(values, torch.Tensor) or values.dim() != 2:
+        raise ValueError("values: expected a matrix (n x k)")
+    k = values.shape[1]
+    _on_device(logits.device, values, index, t_lse, rows, *others)
+    f32 = torch.float32
+    lead = (logits.data_ptr(), _DT[logits.dtype], n, vocab, ld, _flat(values, n * k, f32, "values"),
+            _flat(index, n * k, torch.int32, "index"), _flat(t_lse, n, f32, "t_lse"), k, temperature)
+    return lead, _flat(rows, n, f32, name)
+
+
+def _distill_grad_out(logits, grad, stream):
+    n, vocab = logits.shape
+    if grad is None:
+        return _empty((n, vocab), logits.dtype, logits.device, stream), vocab
+    rows, _, ldg = _rows(grad, "grad", vocab, (logits.dtype,))
+    if rows != n:
+        raise ValueError(f"grad: expected {n} rows, got {rows}")
+    return grad, ldg
+
+
+def kq_distill_loss(logits, values, index, t_lse=None, temperature: float = 1.0, weight=None, stream=None):
+    """Each row's KL divergence from the teacher's list (kq_top_logits) to the
+    student's softmax(logits / T), times weight T^2 (see kq.h). Returns (loss
+    fp32 n, stats fp32 n x 3 for kq_distill_grad)."""
+    lead, pw = _distill_args(logits, values, index, t_lse, temperature, weight, "weight")
+    n, dev = logits.shape[0], logits.device
+    loss = _empty((n,), torch.float32, dev, stream)
+    stats = _empty((n, 3), torch.float32, dev, stream)
+    check(N.lib.kq_distill_loss(*lead, pw, loss.data_ptr(), stats.data_ptr(), _raw_stream(stream, dev)))
+    return loss, stats
+
+
+def kq_distill_grad(logits, values, index, stats, dloss, t_lse=None, temperature: float = 1.0, grad=None,
+                    stream=None):
+    """The gradient in the logits, given the forward call's stats and the
+    gradient dloss (n) of its losses. grad may be the logits themselves."""
+    lead, pd = _distill_args(logits, values, index, t_lse, temperature, dloss, "dloss", stats, grad)
+    if pd is None:
+        raise ValueError("dloss: expected a tensor")
+    n, dev = logits.shape[0], logits.device
+    ps = _flat(stats, 3 * n, torch.float32, "stats")
+    grad, ldg = _distill_grad_out(logits, grad, stream)
+    check(N.lib.kq_distill_grad(*lead, ps, pd, grad.data_ptr(), ldg, _raw_stream(stream, dev)))
+    return grad
+
+
+def kq_distill_loss_grad(logits, values, index, t_lse=None, temperature: float = 1.0, weight=None, grad=None,
+                         stream=None):
+    """(loss n, gradient n x vocab of the sum of the losses) in one pass. grad
+    may be the logits themselves."""
+    lead, pw = _distill_args(logits, values, index, t_lse, temperature, weight, "weight", grad)
+    n, dev = logits.shape[0], logits.device
+    loss = _empty((n,), torch.float32, dev, stream)
+    grad, ldg = _distill_grad_out(logits, grad, stream)
+    check(N.lib.kq_distill_loss_grad(*lead, pw, loss.data_ptr(), None, grad.data_ptr(), ldg,
+                                     _raw_stream(stream, dev)))
+    return loss, grad

@@ -245,6 +245,13 @@ kq_status kq_workspace_size(kq_op op, int64_t d_out, int64_t d_in, int64_t n_tok
       if (d_out < 1 || n_tok < 1) return fail(KQ_ERR_SHAPE, "workspace_size: bad sizes");
       *bytes = apply_a4_ws_bytes(d_out, d_in, n_tok);
       return KQ_OK;
+    case KQ_OP_MATMUL_I8:
+    case KQ_OP_LINEAR_I8:
+      if (d_out < 1 || n_tok < 0) return fail(KQ_ERR_SHAPE, "workspace_size: bad sizes");
+      if (n_tok == 0) return KQ_OK;
+      *bytes = op == KQ_OP_MATMUL_I8 ? matmul_i8_ws_bytes(d_out, d_in, n_tok)
+                                     : linear_i8_ws_bytes(d_out, d_in, n_tok);
+      return KQ_OK;
   }
   return fail(KQ_ERR_ARG, "workspace_size: unknown op %d", int(op));
 }

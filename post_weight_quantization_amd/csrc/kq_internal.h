@@ -168,6 +168,34 @@ kq_status apply_run(const uint32_t* packed, int bits, const float* scale, const 
                     const int8_t* so, int64_t bi, int64_t bo, const float* x, int64_t batch,
                     int64_t d_out, int64_t d_in, float* y, Arena& ws, hipStream_t s);
 
+// ------------------------------------------------------------- 8-bit product
+int64_t i8_row_bytes(int64_t d_in);
+kq_status quantize_rows_run(const void* x, kq_dtype dt, int64_t n, int64_t d, int64_t ldx, float clip,
+                            int8_t* codes, float* scale, int32_t* sums, hipStream_t s);
+kq_status pack_i8_run(const uint8_t* codes, const float* zero, int64_t d_out, int64_t d_in, int8_t* packed,
+                      float* zero_out, hipStream_t s);
+size_t matmul_i8_ws_bytes(int64_t d_out, int64_t d_in, int64_t n);
+kq_status matmul_i8_run(const int8_t* a, const float* a_scale, const int32_t* a_sum, const int8_t* w,
+                        const float* w_scale, const float* w_zero, const float* bias, int64_t n,
+                        int64_t d_out, int64_t d_in, void* y, kq_dtype dt, int64_t ldy, Arena& ws,
+                        hipStream_t s);
+size_t linear_i8_ws_bytes(int64_t d_out, int64_t d_in, int64_t n);
+kq_status linear_i8_run(const void* x, kq_dtype dt, int64_t ldx, float clip, const int8_t* w,
+                        const float* w_scale, const float* w_zero, const float* bias, int64_t n,
+                        int64_t d_out, int64_t d_in, void* y, kq_dtype ydt, int64_t ldy, Arena& ws,
+                        hipStream_t s);
+
+// --------------------------------------------------- top logits, distillation
+int64_t distill_max_vocab();
+int32_t logits_max_k();
+kq_status top_logits_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld, int k,
+                         float temperature, float* values, int32_t* index, float* lse, hipStream_t s);
+// loss: NULL for the gradient from stats; grad: NULL for the loss alone
+kq_status distill_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld,
+                      const float* t_values, const int32_t* t_index, const float* t_lse, int k,
+                      float temperature, const float* weight, float* loss, float* stats, void* grad,
+                      int64_t ldg, hipStream_t s);
+
 __host__ __device__ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace kq

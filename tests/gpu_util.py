@@ -63,3 +63,12 @@ def tile_rel_fro(a, b, t: int) -> float:
             ra = np.linalg.norm(a[i:i + t, j:j + t] - b[i:i + t, j:j + t])
             worst = max(worst, ra / rb if rb > 0 else (0.0 if ra == 0 else np.inf))
     return float(worst)
+
+
+def bf16(a):
+    """Rounded to the nearest bfloat16 (ties to even), as fp64; infinities and
+    NaN stay."""
+    import oracle
+    with np.errstate(over="ignore", invalid="ignore"):
+        f = np.asarray(a, np.float64).astype(np.float32)
+    return np.where(np.isfinite(f), oracle.bf16_rne(f), f).astype(np.float64)
