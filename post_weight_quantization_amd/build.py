@@ -20,7 +20,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkq.so")
 
 SOURCES = ["kq_api.hip", "gemm_f32.hip", "cov.hip", "biip.hip", "chol.hip", "gptaq.hip",
-           "objective.hip", "deploy.hip", "yaqa.hip", "kq_api_head.hip", "i8.hip", "logits.hip"]
+           "objective.hip", "deploy.hip", "yaqa.hip", "kq_api_head.hip", "i8.hip", "top.hip",
+           "distill.hip"]
 
 # microbenchmarks of the part's own ceilings, for the benchmark (not the ABI)
 PEAKS_SOURCES = ["peaks.hip"]

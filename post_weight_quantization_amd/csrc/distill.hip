@@ -1,0 +1,255 @@
+// The distillation loss on a teacher's top logits, and its gradient.
+//
+// With q = softmax(s / T) over the vocabulary and the teacher's probabilities
+// p_k of its K listed columns (renormalised over the list, or
+// exp(t_k / T - Z_t) with everything off the list as one bucket of mass
+// r = 1 - sum p against the student's q_r),
+//   L = w T^2 [ sum_k p_k (log p_k - log q_k) + r (log r - log q_r) ]
+//   dL/ds_j = w T [ c_j q_j - p_j ],   c_j = P on the list, P - r / q_r off it,
+//   P = sum p + r.
+//
+// A workgroup holds its row on chip (logits_rows.h), so the logits are read
+// once and the gradient written once: the largest logit m, the sum of
+// e_j = exp((s_j - m) / T), and e_j again times one factor of the row,
+//   w T (P / sum e - r / sum of e off the list),
+// which is the gradient of every column off the list; the K columns on it
+// are written again after a barrier. The teacher's side is computed by the
+// first K threads while the row is on its way.
+//
+// What decides a small loss is kept from cancelling: m goes off before the
+// scaling, e is summed apart for the columns on and off the list (a bit per
+// column in LDS says which), never as a difference of sums, and the remainder
+// 1 - sum p, the sum of the loss's terms and the factors of the gradient are
+// joined in 64 bits. Exponentials and logarithms are the hardware's in fp32.
+#include "logits_rows.h"
+
+namespace kq {
+
+using namespace rows;
+
+namespace {
+
+constexpr int K_MAX = 256;          // longest list
+constexpr int V_MAX = 1 << 19;      // largest vocabulary: its bits fill 64 KB
+constexpr double REST_MIN = 1.0 / 65536.0;
+constexpr float LOG2E = 1.44269504088896340736f;
+constexpr double LN2 = 0.69314718055994530942;
+
+// a value that all lanes share, in a scalar register
+__device__ inline float uniform(float v) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
+}
+
+__device__ inline float masked(float v, uint32_t keep) { return __uint_as_float(__float_as_uint(v) & keep); }
+
+struct DistillArgs {
+  int64_t n, ld, ldg;
+  int vocab, k;
+  const float* t_values;
+  const int32_t* t_index;
+  const float* t_lse;   // NULL: renormalise over the list
+  float temperature;
+  const float* weight;  // NULL: ones
+  float* loss;
+  float* stats;         // n x 3: m, log sum exp((s - m) / T), log of the mass off the list
+};
+
+template <class T, int CH, int TPB, bool LOSS, bool GRAD>
+__global__ __launch_bounds__(TPB, min_waves(CH)) void distill_kernel(const T* logits, DistillArgs d, T* grad) {
+  extern __shared__ uint32_t bits[];  // a bit per column: on the list
+  __shared__ double dpart[2][TPB / 64];
+  __shared__ float fpart[5][TPB / 64];
+  __shared__ __align__(16) int idx_at[K_MAX];
+  __shared__ __align__(16) float p_at[K_MAX];
+  static_assert(K_MAX <= TPB, "one thread per entry of the list");
+  const int t = threadIdx.x;
+  const int full = d.vocab / E<T>;
+  const float inv_t = 1.f / d.temperature, c = LOG2E / d.temperature;
+  const bool bucket = d.t_lse != nullptr;
+  if (bucket)
+    for (int j = t; j < int(cdiv(d.vocab, 32)); j += TPB) bits[j] = 0;
+  for (int j = t; j < K_MAX; j += TPB) idx_at[j] = -1, p_at[j] = 0.f;
+  __syncthreads();
+  Row<T, CH, TPB> r;
+  r.clear();
+  r.load(logits + int64_t(blockIdx.x) * d.ld, full, d.vocab);
+  for (int64_t row = blockIdx.x; row < d.n; row += gridDim.x) {
+    const T* lr = logits + row * d.ld;
+    T* gr = GRAD ? grad + row * d.ldg : nullptr;
+    const bool more = row + gridDim.x < d.n;
+    const int ahead = more ? full : 0;
+    const T* nr = lr + (more ? int64_t(gridDim.x) * d.ld : 0);
+    const float w = d.weight ? uniform(d.weight[row]) : 1.f;
+    // a row without weight goes along (whatever its logits hold), and zeros
+    // are written for it
+    const uint32_t keep = w == 0.f ? 0u : ~0u;
+    // ---- the teacher's side
+    int idx = -1;
+    float at_idx = 0.f;  // the student's logit there
+    float tv = -__builtin_inff();
+    if (t < d.k) {
+      idx = d.t_index[row * d.k + t];
+      if (uint32_t(idx) >= uint32_t(d.vocab)) idx = -1;
+      idx_at[t] = idx;
+      if (idx >= 0) {
+        at_idx = to_f32(lr[idx]);
+        tv = d.t_values[row * d.k + t];
+        if (bucket) atomicOr(&bits[idx >> 5], 1u << (idx & 31));
+      }
+    }
+    double mass = 1.0, rest = 0.0;
+    float log_p;  // to base 2
+    if (bucket) {
+      // t / T - Z in one rounding
+      log_p = fmaf(tv, inv_t, -d.t_lse[row]) * LOG2E;
+    } else {
+      float tm = block_reduce<TPB>(tv, fpart[3], Max());
+      if (tm == -__builtin_inff()) tm = 0.f;
+      const float z = (tv - tm) * c;
+      const float total = block_reduce<TPB>(__builtin_amdgcn_exp2f(z), fpart[4], Sum());
+      log_p = z - __builtin_amdgcn_logf(total);
+      if (total == 0.f) mass = 0.0;
+    }
+    const float p = idx >= 0 ? __builtin_amdgcn_exp2f(log_p) : 0.f;
+    if (t < d.k) p_at[t] = p;
+    if (bucket) {
+      mass = block_reduce<TPB>(double(p), dpart[0], Sum());
+      rest = 1.0 - mass;
+      if (rest <= REST_MIN) rest = 0.0;
+      mass += rest;
+    } else {
+      __syncthreads();
+    }
+    // entries of one column: the first writes for all
+    float p_col = 0.f;
+    bool writes = GRAD && idx >= 0;
+    if (writes) {
+      for (int l = 0; l < d.k; l += 4) {
+        const int4 other = *reinterpret_cast<const int4*>(idx_at + l);
+        const float4 po = *reinterpret_cast<const float4*>(p_at + l);
+        p_col += (other.x == idx ? po.x : 0.f) + (other.y == idx ? po.y : 0.f) +
+                 (other.z == idx ? po.z : 0.f) + (other.w == idx ? po.w : 0.f);
+        if ((other.x == idx && l < t) || (other.y == idx && l + 1 < t) || (other.z == idx && l + 2 < t) ||
+            (other.w == idx && l + 3 < t))
+          writes = false;
+      }
+    }
+    // ---- the student's side
+    auto on_list = [&](int ch) {
+      const int j = ch * E<T>;
+      return bits[j >> 5] >> (j & 31) & ((1u << E<T>) - 1);
+    };
+    float m, total, off;
+    if (LOSS) {
+      m = r.tail;
+      r.each(lr, full, [&](int, int, const float(&x)[E<T>], const Raw&) {
+        const float top = max_of(x);
+        m = max3(m, top, top);
+      });
+      m = block_reduce<TPB>(m, fpart[0], Max());
+      if (m == -__builtin_inff()) m = 0.f;
+      float on = 0.f;
+      off = 0.f;
+      r.each(lr, full, [&](int reg, int ch, const float(&x)[E<T>], const Raw&) {
+        float e[E<T>], part = 0.f;
+        for (int i = 0; i < E<T>; ++i) part += e[i] = __builtin_amdgcn_exp2f((x[i] - m) * c);
+        const uint32_t mark = bucket && ch < full ? on_list(ch) : 0;
+        if (mark) {
+          part = 0.f;
+          for (int i = 0; i < E<T>; ++i) {
+            if (mark >> i & 1) on += e[i];
+            else part += e[i];
+          }
+        }
+        off += part;
+        if constexpr (CH > 0 && !GRAD) r.load_chunk(reg, nr, ahead);
+      });
+      const int j = full * E<T> + t;
+      const float e = __builtin_amdgcn_exp2f((r.tail - m) * c);
+      if (!GRAD && more) r.load_tail(nr, full, d.vocab);
+      if (bucket && j < d.vocab && bits[j >> 5] >> (j & 31) & 1) on += e;
+      else off += e;
+      off = block_reduce<TPB>(off, fpart[1], Sum());
+      on = block_reduce<TPB>(on, fpart[2], Sum());
+      total = on + off;
+      // to base 2; a row without a finite logit has q = 0 and log q = -inf
+      const float log_total = total == 0.f ? 0.f : __builtin_amdgcn_logf(total);
+      const float log_off = total == 0.f ? -__builtin_inff() : __builtin_amdgcn_logf(off) - log_total;
+      double term = 0.0;
+      if (p > 0.f) term = double(p) * ((double(log_p) - double(at_idx - m) * double(c)) + double(log_total));
+      term = block_reduce<TPB>(term, dpart[1], Sum());
+      if (t == 0) {
+        if (rest > 0.0) term += rest * (double(__builtin_amdgcn_logf(float(rest))) - double(log_off));
+        d.loss[row] = masked(float(double(w) * d.temperature * d.temperature * LN2 * term), keep);
+        if (d.stats) {
+          d.stats[3 * row] = masked(m, keep);
+          d.stats[3 * row + 1] = masked(total == 0.f ? -__builtin_inff() : log_total * float(LN2), keep);
+          d.stats[3 * row + 2] = masked(log_off * float(LN2), keep);
+        }
+      }
+    } else {
+      m = d.stats[3 * row];
+      const float log_total = d.stats[3 * row + 1] * LOG2E, log_off = d.stats[3 * row + 2] * LOG2E;
+      total = __builtin_amdgcn_exp2f(log_total);
+      off = __builtin_amdgcn_exp2f(log_total + log_off);
+    }
+    // ---- the gradient
+    if (GRAD) {
+      const double gain = double(w) * d.temperature;
+      const float f_on = float(total == 0.f ? 0.0 : gain * mass / total);
+      const float f_off = rest > 0.0 && off > 0.f ? float(gain * (mass / total - rest / off)) : f_on;
+      r.each(lr, full, [&](int i, int ch, const float(&x)[E<T>], const Raw&) {
+        float g[E<T>];
+        for (int e = 0; e < E<T>; ++e) g[e] = __builtin_amdgcn_exp2f((x[e] - m) * c) * f_off;
+        Raw q = pack(g);
+        for (uint32_t& word : q.w) word &= keep;
+        if (ch < full) *reinterpret_cast<Raw*>(CH > 0 ? r.chunk_at(gr, i) : gr + int64_t(ch) * E<T>) = q;
+        if constexpr (CH > 0) r.load_chunk(i, nr, ahead);
+      });
+      if (full * E<T> + t < d.vocab)
+        put(gr + full * E<T> + t, masked(__builtin_amdgcn_exp2f((r.tail - m) * c) * f_off, keep));
+      if (more) r.load_tail(nr, full, d.vocab);
+      __syncthreads();
+      if (writes)
+        put(gr + idx, masked(__builtin_amdgcn_exp2f((at_idx - m) * c) * f_on - float(gain) * p_col, keep));
+    } else {
+      __syncthreads();
+    }
+    if (bucket && idx >= 0) bits[idx >> 5] = 0;
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+int64_t distill_max_vocab() { return V_MAX; }
+
+kq_status distill_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld,
+                      const float* t_values, const int32_t* t_index, const float* t_lse, int k,
+                      float temperature, const float* weight, float* loss, float* stats, void* grad,
+                      int64_t ldg, hipStream_t s) {
+  const DistillArgs d{n, ld, ldg, int(vocab), k, t_values, t_index, t_lse, temperature, weight, loss, stats};
+  // the bits are of use with the bucket alone
+  const size_t lds = t_lse ? size_t(cdiv(vocab, 32)) * 4 : 0;
+  auto launch = [&](auto* p) {
+    using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    return with_variant(cdiv(vocab, E<T>), [&](auto v) -> kq_status {
+      using V = decltype(v);
+      auto go = [&](auto kernel) -> kq_status {
+        if (lds > 49152)
+          KQ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)));
+        kernel<<<row_groups<V>(n), V::TPB, lds, s>>>(p, d, static_cast<T*>(grad));
+        KQ_HIP(hipGetLastError());
+        return KQ_OK;
+      };
+      if (loss && grad) return go(distill_kernel<T, V::CH, V::TPB, true, true>);
+      if (loss) return go(distill_kernel<T, V::CH, V::TPB, true, false>);
+      return go(distill_kernel<T, V::CH, V::TPB, false, true>);
+    });
+  };
+  if (dt == KQ_BF16) return launch(static_cast<const uint16_t*>(logits));
+  return launch(static_cast<const float*>(logits));
+}
+
+}  // namespace kq

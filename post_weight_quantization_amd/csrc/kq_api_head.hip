@@ -147,7 +147,7 @@ kq_status kq_top_logits(const void* logits, kq_dtype dt, int64_t n, int64_t voca
                         float temperature, float* values, int32_t* index, float* lse, hipStream_t stream) {
   clear_error();
   KQ_TRY(check_logits(dt, n, vocab, ld, k, temperature, "top_logits"));
-  if (k > vocab || vocab > INT32_MAX) return fail(KQ_ERR_SHAPE, "top_logits: k <= vocab <= 2^31 - 1");
+  if (k > vocab || vocab > (int64_t(1) << 30)) return fail(KQ_ERR_SHAPE, "top_logits: k <= vocab <= 2^30");
   if (n == 0) return KQ_OK;
   if (!logits || !values || !index) return fail(KQ_ERR_ARG, "top_logits: NULL argument");
   if (!aligned(logits, elem(dt))) return fail(KQ_ERR_ARG, "top_logits: logits must be aligned to their type");

@@ -1,0 +1,259 @@
+// A teacher's top logits: the K largest logits of each row in descending
+// order, equal ones by lowest index, and log sum exp(l / T) of the whole row.
+//
+// A workgroup holds its row on chip (logits_rows.h) and goes through it twice.
+//   1. Each thread's largest values over its chunks (a few, of as many
+//      interleaved shares of them): up to 1024 group maxima. The K-th
+//      largest of these, tau, has at least K elements at or above it, and few
+//      more: the groups interleave over the row, so the K largest elements
+//      seldom share one (64 of 1024 groups: 66 elements on average).
+//      Only the upper 16 bits of tau's key are sought, 4 bits a round, the
+//      waves counting for 16 pivots side by side.
+//   2. Chunks with an element at or above tau are appended to LDS, while
+//      the exponentials are summed; their elements at or above tau then make
+//      a list. An element is the 64-bit key (order of its value, complement
+//      of its index), so no two are equal, and its rank is the number of
+//      larger keys on the list.
+// Should either overflow (512 chunks, 1024 elements: many equal logits), a
+// second pass takes what is above tau and, of the first K columns, what equals it:
+// enough if everything else is at or above tau, as in a row whose mask
+// leaves few columns. What that does not settle (and a row with a NaN or +inf) is
+// searched bit by bit for the K-th largest key, counting.
+#include "logits_rows.h"
+
+namespace kq {
+
+using namespace rows;
+
+namespace {
+
+constexpr int K_MAX = 256;        // longest list
+constexpr int CHUNKS = 512;       // chunks with a candidate, in LDS
+constexpr int LIST = 1024;        // candidates in LDS
+constexpr int GROUPS = 1024;      // group maxima
+
+// Order of logits as unsigned keys: -inf lowest, both zeros equal, a NaN
+// above everything.
+__device__ inline uint32_t key_of(float v) {
+  if (v != v) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ inline float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+constexpr uint32_t KEY_NEG_INF = 0x007fffffu;
+
+__device__ inline uint64_t entry_of(float v, int j) { return uint64_t(key_of(v)) << 32 | uint32_t(~uint32_t(j)); }
+
+struct TopLds {
+  uint64_t list[LIST];
+  uint32_t rank[LIST];
+  Raw chunk[CHUNKS];
+  int chunk_no[CHUNKS];
+  uint16_t group[GROUPS];
+  int pivots[2][16];
+  float part[16];
+  int ipart[2][16];
+  int count, chunks;
+};
+
+// Appends the entries among this thread's elements that `take` names.
+template <class T, int TPB, class F>
+__device__ inline void gather(const T* row, int vocab, TopLds& s, F take) {
+#pragma unroll 1
+  for (int j = threadIdx.x; j < vocab; j += TPB) {
+    const float v = to_f32(row[j]);
+    if (take(v, j)) {
+      const int at = atomicAdd(&s.count, 1);
+      if (at < LIST) s.list[at] = entry_of(v, j);
+    }
+  }
+}
+
+// The exact search: the K-th largest key by its bits, then, among the
+// elements of that key, the index up to which they belong to the K.
+template <class T, int TPB>
+__device__ void search(const T* row, int vocab, int k, TopLds& s) {
+  auto count = [&](int flip, auto f) {
+    int c = 0;
+#pragma unroll 1
+    for (int j = threadIdx.x; j < vocab; j += TPB) c += f(key_of(to_f32(row[j])), j);
+    return block_reduce<TPB>(c, s.ipart[flip & 1], Sum());
+  };
+  uint32_t key = 0;
+  int flip = 0;
+  // a bfloat16's key has ones or zeros alone in its lower half
+#pragma unroll 1
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t probe = key | 1u << b;
+    if (count(flip++, [&](uint32_t q, int) { return int(q >= probe); }) >= k) key = probe;
+  }
+  const int above = count(flip++, [&](uint32_t q, int) { return int(q > key); });
+  // the lowest bound such that enough elements of this key lie below it
+  int bound = 0;
+#pragma unroll 1
+  for (int b = 30; b >= 0; --b) {
+    const int probe = bound | 1 << b;
+    if (probe <= vocab &&
+        count(flip++, [&](uint32_t q, int j) { return int(q == key && j < probe); }) < k - above)
+      bound = probe;
+  }
+  if (threadIdx.x == 0) s.count = 0;
+  __syncthreads();
+  gather<T, TPB>(row, vocab, s, [&](float v, int j) {
+    const uint32_t q = key_of(v);
+    return q > key || (q == key && j <= bound);
+  });
+  __syncthreads();
+}
+
+template <class T, int CH, int TPB>
+__global__ __launch_bounds__(TPB, min_waves(CH)) void top_logits_kernel(const T* __restrict__ logits, int64_t n, int vocab,
+                                                         int64_t ld, int k, float inv_t,
+                                                         float* __restrict__ values,
+                                                         int32_t* __restrict__ index,
+                                                         float* __restrict__ lse) {
+  constexpr int GP = GROUPS / TPB;  // groups of a thread
+  constexpr int NW = TPB / 64;
+  __shared__ TopLds s;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  const int full = vocab / E<T>;
+  const float c = inv_t * 1.44269504088896340736f;
+  Row<T, CH, TPB> r;
+  r.clear();
+  r.load(logits + int64_t(blockIdx.x) * ld, full, vocab);
+  for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
+    const T* lr = logits + row * ld;
+    const bool more = row + gridDim.x < n;
+    const int ahead = more ? full : 0;
+    const T* nr = lr + (more ? int64_t(gridDim.x) * ld : 0);
+    // ---- the largest of each group
+    float g[GP];
+    for (int i = 0; i < GP; ++i) g[i] = -__builtin_inff();
+    r.each(lr, full, [&](int i, int, const float(&x)[E<T>], const Raw&) {
+      const float top = max_of(x);
+      g[i % GP] = max3(g[i % GP], top, top);
+    });
+    g[0] = max3(g[0], r.tail, r.tail);
+    float m = g[0];
+    for (int i = 1; i < GP; ++i) m = max3(m, g[i], g[i]);
+    for (int i = 0; i < GP; ++i) s.group[i * TPB + t] = uint16_t(key_of(g[i]) >> 16);
+    if (t == 0) s.count = 0, s.chunks = 0;
+    m = block_reduce<TPB>(m, s.part, Max());
+    // ---- the K-th largest of them, from the top in steps of 4 bits
+    uint32_t key = 0;
+    {
+      uint32_t v[GROUPS / 64];
+      for (int i = 0; i < GROUPS / 64; ++i) v[i] = s.group[i * 64 + lane];
+#pragma unroll 1
+      for (int step = 0; step < 4; ++step) {
+#pragma unroll 1
+        for (int p = w; p < 16; p += NW) {
+          const uint32_t pivot = key + (uint32_t(p) << (12 - 4 * step));
+          int cnt = 0;
+          for (int i = 0; i < GROUPS / 64; ++i) cnt += __popcll(__ballot(v[i] >= pivot));
+          if (lane == 0) s.pivots[step & 1][p] = cnt;
+        }
+        __syncthreads();
+        int best = 0;
+        for (int p = 1; p < 16; ++p) best = s.pivots[step & 1][p] >= k ? p : best;
+        key += uint32_t(best) << (12 - 4 * step);
+      }
+    }
+    // too few groups reach above -inf: so does tau
+    const float tau = key <= (KEY_NEG_INF >> 16) ? -__builtin_inff() : value_of(key << 16);
+    // ---- candidates, and the sum of exponentials
+    const float ref = m == -__builtin_inff() ? 0.f : m;
+    float sum = 0.f;
+    auto append = [&](float v, int j) {
+      const int at = atomicAdd(&s.count, 1);
+      if (at < LIST) s.list[at] = entry_of(v, j);
+    };
+    r.each(lr, full, [&](int i, int ch, const float(&x)[E<T>], const Raw& q) {
+      if (max_of(x) >= tau && ch < full) {
+        const int at = atomicAdd(&s.chunks, 1);
+        if (at < CHUNKS) s.chunk[at] = q, s.chunk_no[at] = ch;
+      }
+      float part = 0.f;
+      for (int e = 0; e < E<T>; ++e) part += __builtin_amdgcn_exp2f((x[e] - ref) * c);
+      sum += part;
+      // computed here, not where the sum is used: the elements would be kept
+      asm volatile("" : "+v"(sum));
+      if constexpr (CH > 0)
+        r.load_chunk(i, nr, ahead);
+    });
+    if (r.tail >= tau && full * E<T> + t < vocab) append(r.tail, full * E<T> + t);
+    sum += __builtin_amdgcn_exp2f((r.tail - ref) * c);
+    if (more) r.load_tail(nr, full, vocab);
+    sum = block_reduce<TPB>(sum, s.part, Sum());
+    const int chunks = s.chunks;
+#pragma unroll 1
+    for (int i = t; i < (chunks < CHUNKS ? chunks : CHUNKS) * E<T>; i += TPB) {
+      const Raw q = s.chunk[i / E<T>];
+      float x[E<T>];
+      unpack(q, x);
+      float v = x[0];
+      for (int e = 1; e < E<T>; ++e) v = i % E<T> == e ? x[e] : v;
+      if (v >= tau) append(v, s.chunk_no[i / E<T>] * E<T> + i % E<T>);
+    }
+    __syncthreads();
+    if (lse && t == 0) lse[row] = ref * inv_t + logf(sum);
+    int count = s.count;
+    if (chunks > CHUNKS || count > LIST || sum != sum) {
+      __syncthreads();
+      if (t == 0) s.count = 0;
+      __syncthreads();
+      gather<T, TPB>(lr, vocab, s, [&](float v, int j) { return v > tau || (v == tau && j < k); });
+      __syncthreads();
+      count = s.count;
+      if (count > LIST || count < k || sum != sum) {
+        search<T, TPB>(lr, vocab, k, s);
+        count = s.count;
+      }
+    }
+    // ---- ranks: threads t, t + width, ... share the comparisons of one candidate
+    int width = 64;
+    while (width < count && width < TPB) width *= 2;
+#pragma unroll 1
+    for (int i = t; i < count; i += TPB) s.rank[i] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = t & (width - 1); i < count; i += width) {
+      const uint64_t mine = s.list[i];
+      uint32_t before = 0;
+      for (int j = t / width; j < count; j += TPB / width) before += s.list[j] > mine;
+      if (before) atomicAdd(&s.rank[i], before);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = t; i < count; i += TPB) {
+      const uint32_t at = s.rank[i];
+      if (at < uint32_t(k)) {
+        values[row * k + at] = value_of(uint32_t(s.list[i] >> 32));
+        index[row * k + at] = int32_t(~uint32_t(s.list[i]));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+int32_t logits_max_k() { return K_MAX; }
+
+kq_status top_logits_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld, int k,
+                         float temperature, float* values, int32_t* index, float* lse, hipStream_t s) {
+  auto launch = [&](auto* p) {
+    using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    return with_variant(cdiv(vocab, E<T>), [&](auto v) -> kq_status {
+      using V = decltype(v);
+      top_logits_kernel<T, V::CH, V::TPB><<<row_groups<V>(n), V::TPB, 0, s>>>(
+          p, n, int(vocab), ld, k, 1.f / temperature, values, index, lse);
+      KQ_HIP(hipGetLastError());
+      return KQ_OK;
+    });
+  };
+  if (dt == KQ_BF16) return launch(static_cast<const uint16_t*>(logits));
+  return launch(static_cast<const float*>(logits));
+}
+
+}  // namespace kq

@@ -117,7 +117,7 @@ CASES = [
     ("top k 0", lambda: top(k=0), SHAPE, "k"),
     ("top k 257", lambda: top(k=257, v=1000, ld=1000), SHAPE, "256"),
     ("top k above vocab", lambda: top(k=101), SHAPE, "k <= vocab"),
-    ("top vocab above int32", lambda: top(v=1 << 31, ld=1 << 31), SHAPE, "2^31"),
+    ("top vocab above int32", lambda: top(v=1 << 31, ld=1 << 31), SHAPE, "2^30"),
     ("top temperature 0", lambda: top(t=0.0), ARG, "temperature"),
     ("top temperature inf", lambda: top(t=math.inf), ARG, "temperature"),
     ("top null", lambda: top(idx=None), ARG, "NULL"),
