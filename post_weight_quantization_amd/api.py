@@ -8,6 +8,7 @@ the current HIP stream. Every step of the computation runs in libkq's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import numpy as np
 import torch
@@ -405,6 +406,12 @@ def _raw_stream(stream, device):
     return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
+@functools.lru_cache(maxsize=1024)
+def _need(op, d_out, d_in, n):
+    """kq_workspace_size: of the sizes alone, so looked up once for each."""
+    return kq_workspace_size(op, d_out, d_in, n)
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor in the memory of the stream that the call runs on: no
     earlier work of another stream can still be using that memory."""
@@ -447,8 +454,9 @@ def _flat(t, count, dtype, name):
 def _on_device(device, *ts):
     if device.type != "cuda":
         raise ValueError("tensors must be on the GPU")
+    index = device.index
     for t in ts:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"tensors must be on one GPU, got {device} and {t.device}")
 
 
@@ -460,8 +468,8 @@ def kq_i8_row_bytes(d_in: int) -> int:
 
 
 def _codes(t, rows, d_in, name):
-    rb = kq_i8_row_bytes(d_in)
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int8 or tuple(t.shape) != (rows, rb) or \
+    rb = (d_in + 127) // 128 * 128
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int8 or t.shape != (rows, rb) or \
             not t.is_contiguous():
         got = f"{tuple(t.shape)} {t.dtype}" if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name}: expected contiguous int8 codes {(rows, rb)}, got {got}")
@@ -526,7 +534,7 @@ def kq_matmul_i8(a, a_scale, w, w_scale, d_in: int, a_sum=None, w_zero=None, bia
     f32 = torch.float32
     y, ldy = _product_out(y, n, d_out, dtype, dev, stream)
     if ws is None:
-        need = kq_workspace_size(N.KQ_OP_MATMUL_I8, d_out, d_in, n)
+        need = _need(N.KQ_OP_MATMUL_I8, d_out, d_in, n)
         ws = _empty((need,), torch.uint8, dev, stream) if need else None
     check(N.lib.kq_matmul_i8(pa, _flat(a_scale, n, f32, "a_scale"), _flat(a_sum, n, torch.int32, "a_sum"), pw,
                              _flat(w_scale, d_out, f32, "w_scale"), _flat(w_zero, d_out, f32, "w_zero"),
@@ -549,7 +557,7 @@ def kq_linear_i8(x, w, w_scale, w_zero=None, bias=None, clip: float = 1.0, y=Non
     f32 = torch.float32
     y, ldy = _product_out(y, n, d_out, dtype or x.dtype, dev, stream)
     if ws is None:
-        ws = _empty((kq_workspace_size(N.KQ_OP_LINEAR_I8, d_out, d_in, n),), torch.uint8, dev, stream)
+        ws = _empty((_need(N.KQ_OP_LINEAR_I8, d_out, d_in, n),), torch.uint8, dev, stream)
     check(N.lib.kq_linear_i8(x.data_ptr(), _DT[x.dtype], ldx, clip, pw, _flat(w_scale, d_out, f32, "w_scale"),
                              _flat(w_zero, d_out, f32, "w_zero"), _flat(bias, d_out, f32, "bias"), n, d_out,
                              d_in, y.data_ptr(), _DT[y.dtype], ldy, ws.data_ptr(), _nbytes(ws),

@@ -9,8 +9,8 @@
 //   P = sum p + r.
 //
 // A workgroup holds its row on chip (logits_rows.h), so the logits are read
-// once and the gradient written once: the largest logit m, the sum of
-// e_j = exp((s_j - m) / T), and e_j again times one factor of the row,
+// once and the gradient written once: the largest logit m and the sum of
+// e_j = exp((s_j - m) / T) in one pass, and e_j again times one factor of the row,
 //   w T (P / sum e - r / sum of e off the list),
 // which is the gradient of every column off the list; the K columns on it
 // are written again after a barrier. The teacher's side is computed by the
@@ -54,8 +54,9 @@ struct DistillArgs {
   float* stats;         // n x 3: m, log sum exp((s - m) / T), log of the mass off the list
 };
 
-template <class T, int CH, int TPB, bool LOSS, bool GRAD>
-__global__ __launch_bounds__(TPB, min_waves(CH)) void distill_kernel(const T* logits, DistillArgs d, T* grad) {
+template <class T, class V, bool LOSS, bool GRAD>
+__global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logits, DistillArgs d, T* grad) {
+  constexpr int CH = V::CH, TPB = V::TPB;
   extern __shared__ uint32_t bits[];  // a bit per column: on the list
   __shared__ double dpart[2][TPB / 64];
   __shared__ float fpart[5][TPB / 64];
@@ -70,8 +71,7 @@ __global__ __launch_bounds__(TPB, min_waves(CH)) void distill_kernel(const T* lo
     for (int j = t; j < int(cdiv(d.vocab, 32)); j += TPB) bits[j] = 0;
   for (int j = t; j < K_MAX; j += TPB) idx_at[j] = -1, p_at[j] = 0.f;
   __syncthreads();
-  Row<T, CH, TPB> r;
-  r.clear();
+  Row<T, V> r;
   r.load(logits + int64_t(blockIdx.x) * d.ld, full, d.vocab);
   for (int64_t row = blockIdx.x; row < d.n; row += gridDim.x) {
     const T* lr = logits + row * d.ld;
@@ -141,18 +141,16 @@ __global__ __launch_bounds__(TPB, min_waves(CH)) void distill_kernel(const T* lo
     };
     float m, total, off;
     if (LOSS) {
-      m = r.tail;
-      r.each(lr, full, [&](int, int, const float(&x)[E<T>], const Raw&) {
-        const float top = max_of(x);
-        m = max3(m, top, top);
-      });
-      m = block_reduce<TPB>(m, fpart[0], Max());
-      if (m == -__builtin_inff()) m = 0.f;
-      float on = 0.f;
+      Online o;
+      float on = 0.f, top = max3(r.tail, LOWEST, LOWEST);
       off = 0.f;
-      r.each(lr, full, [&](int reg, int ch, const float(&x)[E<T>], const Raw&) {
+      auto rescale = [&](float f) { on *= f, off *= f; };
+      r.template each<!GRAD>(lr, full, [&](int, int ch, const float(&x)[E<T>], Raw) {
+        const float here = max_of(x);
+        top = max3(top, here, here);
+        o.raise(here, c, rescale);
         float e[E<T>], part = 0.f;
-        for (int i = 0; i < E<T>; ++i) part += e[i] = __builtin_amdgcn_exp2f((x[i] - m) * c);
+        for (int i = 0; i < E<T>; ++i) part += e[i] = __builtin_amdgcn_exp2f((x[i] - o.m) * c);
         const uint32_t mark = bucket && ch < full ? on_list(ch) : 0;
         if (mark) {
           part = 0.f;
@@ -162,16 +160,19 @@ __global__ __launch_bounds__(TPB, min_waves(CH)) void distill_kernel(const T* lo
           }
         }
         off += part;
-        if constexpr (CH > 0 && !GRAD) r.load_chunk(reg, nr, ahead);
       });
+      o.raise(r.tail, c, rescale);
       const int j = full * E<T> + t;
-      const float e = __builtin_amdgcn_exp2f((r.tail - m) * c);
+      const float e = __builtin_amdgcn_exp2f((r.tail - o.m) * c);
       if (!GRAD && more) r.load_tail(nr, full, d.vocab);
       if (bucket && j < d.vocab && bits[j >> 5] >> (j & 31) & 1) on += e;
       else off += e;
+      m = block_reduce<TPB>(top, fpart[0], Max());
+      rescale(__builtin_amdgcn_exp2f((o.m - m) * c));
       off = block_reduce<TPB>(off, fpart[1], Sum());
       on = block_reduce<TPB>(on, fpart[2], Sum());
       total = on + off;
+      if (total == 0.f) m = 0.f;
       // to base 2; a row without a finite logit has q = 0 and log q = -inf
       const float log_total = total == 0.f ? 0.f : __builtin_amdgcn_logf(total);
       const float log_off = total == 0.f ? -__builtin_inff() : __builtin_amdgcn_logf(off) - log_total;
@@ -198,12 +199,12 @@ __global__ __launch_bounds__(TPB, min_waves(CH)) void distill_kernel(const T* lo
       const double gain = double(w) * d.temperature;
       const float f_on = float(total == 0.f ? 0.0 : gain * mass / total);
       const float f_off = rest > 0.0 && off > 0.f ? float(gain * (mass / total - rest / off)) : f_on;
-      r.each(lr, full, [&](int i, int ch, const float(&x)[E<T>], const Raw&) {
+      r.template each<true>(lr, full, [&](int i, int ch, const float(&x)[E<T>], Raw) {
         float g[E<T>];
         for (int e = 0; e < E<T>; ++e) g[e] = __builtin_amdgcn_exp2f((x[e] - m) * c) * f_off;
         Raw q = pack(g);
-        for (uint32_t& word : q.w) word &= keep;
-        if (ch < full) *reinterpret_cast<Raw*>(CH > 0 ? r.chunk_at(gr, i) : gr + int64_t(ch) * E<T>) = q;
+        q &= keep;
+        if (ch < full) store_once(CH > 0 ? r.chunk_at(gr, i) : gr + int64_t(ch) * E<T>, q);
         if constexpr (CH > 0) r.load_chunk(i, nr, ahead);
       });
       if (full * E<T> + t < d.vocab)
@@ -231,22 +232,44 @@ kq_status distill_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab,
   const DistillArgs d{n, ld, ldg, int(vocab), k, t_values, t_index, t_lse, temperature, weight, loss, stats};
   // the bits are of use with the bucket alone
   const size_t lds = t_lse ? size_t(cdiv(vocab, 32)) * 4 : 0;
-  auto launch = [&](auto* p) {
+  auto launch = [&](auto* p) -> kq_status {
     using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
-    return with_variant(cdiv(vocab, E<T>), [&](auto v) -> kq_status {
+    const int64_t chunks = cdiv(vocab, E<T>);
+    auto go = [&](auto v, auto with_loss, auto with_grad) -> kq_status {
       using V = decltype(v);
-      auto go = [&](auto kernel) -> kq_status {
-        if (lds > 49152)
-          KQ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)));
-        kernel<<<row_groups<V>(n), V::TPB, lds, s>>>(p, d, static_cast<T*>(grad));
-        KQ_HIP(hipGetLastError());
-        return KQ_OK;
-      };
-      if (loss && grad) return go(distill_kernel<T, V::CH, V::TPB, true, true>);
-      if (loss) return go(distill_kernel<T, V::CH, V::TPB, true, false>);
-      return go(distill_kernel<T, V::CH, V::TPB, false, true>);
-    });
+      const auto kernel = distill_kernel<T, V, decltype(with_loss)::value, decltype(with_grad)::value>;
+      if (lds > 49152)
+        KQ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)));
+      kernel<<<row_groups<V>(n), V::TPB, lds, s>>>(p, d, static_cast<T*>(grad));
+      KQ_HIP(hipGetLastError());
+      return KQ_OK;
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    // What is chosen goes by the row's length alone, so that a row's sums, and
+    // their rounding, are the same in whatever company.
+    // One pass, nothing to hold: loss of 4096 x 32000 bf16 58 us with 256
+    // threads, 72 with 512; 4096 x 128256: 160, 164 (few rows: 16 x 32000 11, 9).
+    if (!grad) return chunks <= 4096 ? go(Variant<0, 256, 6>(), yes, no) : go(Variant<0, 512, 6>(), yes, no);
+    if (!loss) {
+      // gradient of 8192 x 4000 bf16: 52 us with 256 threads, 75 with 512; 4096
+      // x 32000: 107, 103; 4096 x 128256: 417, 405, 392 with 1024
+      if (chunks <= 2048) return go(Variant<0, 256, 6>(), no, yes);
+      if (chunks <= 8192) return go(Variant<0, 512, 6>(), no, yes);
+      return go(Variant<0, 1024, 8>(), no, yes);
+    }
+    // Loss and gradient: two passes. Rows of up to 128 KB are held in
+    // registers (4096 x 32000 bf16: 119 us, read twice 126; 4096 x 65536: 239,
+    // 256); of longer ones a CU holds too few at once to keep the memory
+    // busy, and the second pass finds them in the cache beside it (4096 x
+    // 128256: 467 us, in registers 581).
+    if (chunks <= 512) return go(Variant<2, 256, 6>(), yes, yes);
+    if (chunks <= 1024) return go(Variant<4, 256, 6>(), yes, yes);
+    if (chunks <= 2048) return go(Variant<8, 256, 5>(), yes, yes);
+    if (chunks <= 4096) return go(Variant<16, 256, 4>(), yes, yes);
+    if (chunks <= 8192) return go(Variant<16, 512, 4>(), yes, yes);
+    return go(Variant<0, 512, 6>(), yes, yes);
   };
   if (dt == KQ_BF16) return launch(static_cast<const uint16_t*>(logits));
   return launch(static_cast<const float*>(logits));

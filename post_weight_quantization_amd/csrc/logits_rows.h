@@ -1,16 +1,15 @@
 // Rows of logits held on chip, shared by the top-logit and the distillation
 // kernels.
 //
-// One workgroup takes a row. Its threads hold the row in registers, CH chunks
-// of 16 bytes each (chunk c of the row is register c / TPB of thread c % TPB,
-// so that a wave's loads are 1 KB of adjacent bytes), and the elements past
-// the last full chunk as one value each of the first threads. The register
-// file of a CU (512 KB) takes the largest rows here, up to 20 chunks a thread
-// of 1024, which are read from memory once, whatever the number of passes
-// over them; longer rows (CH = 0) are read again for each pass. A workgroup goes on to
-// further rows and loads the next one, chunk by chunk, as the last pass
-// frees the registers. Rows need no alignment beyond their element's: global
-// loads and stores of 16 bytes take any.
+// One workgroup takes a row. Its threads may hold the row in registers, CH
+// chunks of 16 bytes each (chunk c of the row is register c / TPB of thread
+// c % TPB, so that a wave's loads are 1 KB of adjacent bytes), and the elements
+// past the last full chunk as one value each of the first threads; the row is
+// then read from memory once, whatever the number of passes over it, and the
+// workgroup loads its next one, chunk by chunk, as the last pass frees the
+// registers. With CH = 0 each pass reads the row, the first from memory, later
+// ones, as a rule, from the cache beside it. Rows need no alignment beyond
+// their element's: global loads and stores of 16 bytes take any.
 #pragma once
 #include "kq_internal.h"
 
@@ -20,9 +19,21 @@ namespace rows {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-struct __attribute__((packed, aligned(2))) Raw {
-  uint32_t w[4];
-};
+// 16 bytes of a row as they lie. One vector of four registers throughout: of
+// four words, the compiler would keep each where it likes, and copy them there
+// as soon as they come.
+typedef uint32_t Raw __attribute__((ext_vector_type(4)));
+typedef uint32_t RawMem __attribute__((ext_vector_type(4), aligned(2)));  // at any element
+
+// What the kernel itself touches once goes past the caches' usual order
+// (reading 2 GB so took 6.5 TB/s, else 5.9; copying them 5.2, else 4.7).
+__device__ __forceinline__ Raw load_once(const void* p) {
+  return __builtin_nontemporal_load(static_cast<const RawMem*>(p));
+}
+__device__ __forceinline__ Raw load_kept(const void* p) { return *static_cast<const RawMem*>(p); }
+__device__ __forceinline__ void store_once(void* p, Raw q) {
+  __builtin_nontemporal_store(RawMem(q), static_cast<RawMem*>(p));
+}
 
 template <class T>
 constexpr int E = 16 / int(sizeof(T));  // elements of a chunk
@@ -39,16 +50,16 @@ __device__ inline uint32_t pack_bf16(float lo, float hi) {
 __device__ inline void put(uint16_t* p, float v) { *p = uint16_t(pack_bf16(v, v)); }
 __device__ inline void put(float* p, float v) { *p = v; }
 
-__device__ inline void unpack(const Raw& r, float (&x)[8]) {
+__device__ inline void unpack(Raw r, float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(r.w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+    x[2 * i] = __uint_as_float(r[i] << 16);
+    x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
   }
 }
-__device__ inline void unpack(const Raw& r, float (&x)[4]) {
+__device__ inline void unpack(Raw r, float (&x)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r.w[i]);
+  for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r[i]);
 }
 __device__ inline Raw pack(const float (&x)[8]) {
   return {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
@@ -81,10 +92,17 @@ template <class T>
 __device__ constexpr uint32_t neg_inf_word() {
   return sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
 }
+static __device__ const uint32_t neg_inf_chunks[2][4] = {{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u},
+                                                         {0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u}};
+template <class T>
+__device__ __forceinline__ const uint32_t* neg_inf_chunk() {
+  return neg_inf_chunks[sizeof(T) == 2 ? 0 : 1];
+}
 
 // The part of a row that thread t holds (see above).
-template <class T, int CH, int TPB>
+template <class T, class V>
 struct Row {
+  static constexpr int CH = V::CH, TPB = V::TPB;
   Raw reg[CH > 0 ? CH : 1];
   float tail;
 
@@ -97,20 +115,19 @@ struct Row {
     char* base = reinterpret_cast<char*>(row) + at;
     return reinterpret_cast<T*>(base + threadIdx.x * 16u);
   }
-  // -inf everywhere; what no load reaches stays so.
-  __device__ __forceinline__ void clear() {
-    constexpr uint32_t ni = neg_inf_word<T>();
-    for (Raw& q : reg) q = {ni, ni, ni, ni};
-    tail = -__builtin_inff();
-  }
-  // Register i <- chunk i of this thread's, of the row's `full` chunks (0:
-  // no load, the register is kept).
+  // Register i <- chunk i of this thread's, of the row's `full` chunks; past
+  // the last one, -inf from a constant. (Loads of some lanes only would have
+  // to be merged with what the others hold, and be waited for on the spot.)
   __device__ __forceinline__ void load_chunk(int i, const T* row, int full) {
-    if (i * TPB + thread_of_row() < full) reg[i] = *reinterpret_cast<const Raw*>(chunk_at(const_cast<T*>(row), i));
+    typedef const __attribute__((address_space(1))) RawMem* Global;  // either: both are global memory
+    const uint64_t at = reinterpret_cast<uint64_t>(chunk_at(const_cast<T*>(row), i));
+    const uint64_t none = reinterpret_cast<uint64_t>(neg_inf_chunk<T>());
+    const bool have = i * TPB + thread_of_row() < full;
+    reg[i] = __builtin_nontemporal_load(reinterpret_cast<Global>(have ? at : none));
   }
   __device__ __forceinline__ void load_tail(const T* row, int full, int vocab) {
     const int j = full * E<T> + int(threadIdx.x);
-    if (j < vocab) tail = to_f32(row[j]);
+    tail = j < vocab ? to_f32(row[j]) : -__builtin_inff();
   }
   __device__ __forceinline__ void load(const T* row, int full, int vocab) {
     if constexpr (CH > 0) {
@@ -122,25 +139,48 @@ struct Row {
   // f(register, chunk, elements, chunk as it lies) for each of this thread's chunks. A pass
   // unpacks them anew (the empty asm hides that they have not changed):
   // kept from pass to pass, the unpacked row would be twice the registers.
-  template <class F>
+  // ONCE: without registers for the row, this is the last pass over it.
+  template <bool ONCE = false, class F>
   __device__ __forceinline__ void each(const T* row, int full, F f) {
     if constexpr (CH > 0) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         Raw& q = reg[i];
-        asm volatile("" : "+v"(q.w[0]), "+v"(q.w[1]), "+v"(q.w[2]), "+v"(q.w[3]));
+        asm volatile("" : "+v"(q));
         float x[E<T>];
         unpack(q, x);
         f(i, i * TPB + thread_of_row(), x, q);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-#pragma unroll 4
-      for (int c = threadIdx.x; c < full; c += TPB) {
+      // every lane goes through every chunk of its wave (past the last one
+      // with -inf), so that what f counts over the wave stays the same in all
+      constexpr int U = V::UNROLL;
+      constexpr uint32_t ni = neg_inf_word<T>();
+      auto take = [&](int at, const Raw& q) {
         float x[E<T>];
-        const Raw q = *reinterpret_cast<const Raw*>(row + int64_t(c) * E<T>);
         unpack(q, x);
-        f(0, c, x, q);
+        f(0, at, x, q);
+      };
+      auto get = [&](int at) {
+        const T* src = row + int64_t(at) * E<T>;
+        if constexpr (ONCE) return load_once(src);
+        else return load_kept(src);
+      };
+      const int lane = int(threadIdx.x) & 63;
+      int first = __builtin_amdgcn_readfirstlane(int(threadIdx.x) & ~63);
+      for (; first + (U - 1) * TPB + 64 <= full; first += U * TPB) {
+        Raw q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = get(first + u * TPB + lane);
+#pragma unroll
+        for (int u = 0; u < U; ++u) take(first + u * TPB + lane, q[u]);
+      }
+      for (; first < full; first += TPB) {
+        const int at = first + lane;
+        Raw q = {ni, ni, ni, ni};
+        if (at < full) q = get(at);
+        take(at, q);
       }
     }
   }
@@ -169,32 +209,41 @@ struct Max {
   __device__ double operator()(double a, double b) const { return a > b ? a : b; }
 };
 
-// Calls go(integral constants CH, TPB) for the variant that holds `chunks`:
-// small rows take small workgroups, several to a CU.
-template <int A, int B>
-struct Variant {
-  static constexpr int CH = A, TPB = B;
-};
-template <class G>
-kq_status with_variant(int64_t chunks, G go) {
-  if (chunks <= 256 * 2) return go(Variant<2, 256>());
-  if (chunks <= 256 * 4) return go(Variant<4, 256>());
-  if (chunks <= 256 * 8) return go(Variant<8, 256>());
-  if (chunks <= 512 * 8) return go(Variant<8, 512>());
-  if (chunks <= 512 * 16) return go(Variant<16, 512>());
-  if (chunks <= 512 * 32) return go(Variant<32, 512>());
-  if (chunks <= 512 * 40) return go(Variant<40, 512>());
-  return go(Variant<0, 512>());
-}
+// What a thread's exponentials are taken against: not its running maximum
+// but a value that the largest so far is at most 2^60 times of (in fp32 sums
+// neither overflow nor lose digits by that), so that it seldom moves: of 64
+// lanes, one or the other has a new maximum at almost every chunk. A chunk
+// is taken when it has come, while later ones are on their way; with a pass
+// for the maximum and one for the sum after it, the memory was idle during
+// the second (loss and gradient of 4096 x 128256 bf16: 618 us so).
+constexpr float LOWEST = -3.402823466e38f;
+struct Online {
+  float m = LOWEST;  // finite: -inf less it is -inf, never NaN
 
-// Waves of a SIMD that the registers of a variant are to leave room for.
-constexpr int min_waves(int ch) { return ch == 0 || ch > 16 ? 2 : 4; }
+  // before the exponentials of elements up to `top`: the factor that the
+  // sums so far take
+  template <class F>
+  __device__ __forceinline__ void raise(float top, float c, F scale) {
+    if ((top - m) * c > 60.f) {
+      scale(__builtin_amdgcn_exp2f((m - top) * c));
+      m = top;
+    }
+  }
+};
+
+// How a kernel takes rows: chunks in a thread's registers, threads of a
+// workgroup, and waves of a SIMD that its registers are to leave room for.
+template <int CH_, int TPB_, int WAVES_>
+struct Variant {
+  static constexpr int CH = CH_, TPB = TPB_, WAVES = WAVES_;
+  static constexpr int UNROLL = 4;
+};
 
 // Workgroups of a launch: as many as the 256 CUs hold at once, so that each
 // goes through its share of the rows.
 template <class V>
 inline unsigned row_groups(int64_t n) {
-  const int64_t at_once = 256 * (4 * min_waves(V::CH) / (V::TPB / 64));
+  const int64_t at_once = 256 * (4 * V::WAVES / (V::TPB / 64));
   return unsigned(n < at_once ? n : at_once);
 }
 

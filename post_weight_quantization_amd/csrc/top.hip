@@ -2,20 +2,23 @@
 // order, equal ones by lowest index, and log sum exp(l / T) of the whole row.
 //
 // A workgroup holds its row on chip (logits_rows.h) and goes through it twice.
-//   1. Each thread's largest values over its chunks (a few, of as many
-//      interleaved shares of them): up to 1024 group maxima. The K-th
+//   1. Each thread's largest value over its chunks (for long lists up to
+//      four, of as many interleaved shares of them): 256 to 1024 group maxima. The K-th
 //      largest of these, tau, has at least K elements at or above it, and few
 //      more: the groups interleave over the row, so the K largest elements
 //      seldom share one (64 of 1024 groups: 66 elements on average).
 //      Only the upper 16 bits of tau's key are sought, 4 bits a round, the
 //      waves counting for 16 pivots side by side.
-//   2. Chunks with an element at or above tau are appended to LDS, while
-//      the exponentials are summed; their elements at or above tau then make
+//   2. Chunks with an element at or above tau go to LDS, each wave's to a
+//      part of its own (places by ballot, no atomics to wait for), while the
+//      exponentials are summed and the next row is loaded in their place (64
+//      of 4096 x 128256 bf16: 268 us; with the sums in the first pass, after
+//      which the loads begin later, 329 us); their elements at or above tau then make
 //      a list. An element is the 64-bit key (order of its value, complement
 //      of its index), so no two are equal, and its rank is the number of
 //      larger keys on the list.
-// Should either overflow (512 chunks, 1024 elements: many equal logits), a
-// second pass takes what is above tau and, of the first K columns, what equals it:
+// Should either overflow (128 chunks of a wave, 1024 elements: many equal
+// logits), a second pass takes what is above tau and, of the first K columns, what equals it:
 // enough if everything else is at or above tau, as in a row whose mask
 // leaves few columns. What that does not settle (and a row with a NaN or +inf) is
 // searched bit by bit for the K-th largest key, counting.
@@ -28,7 +31,7 @@ using namespace rows;
 namespace {
 
 constexpr int K_MAX = 256;        // longest list
-constexpr int CHUNKS = 512;       // chunks with a candidate, in LDS
+constexpr int CHUNKS = 128;       // chunks with a candidate of one wave, in LDS
 constexpr int LIST = 1024;        // candidates in LDS
 constexpr int GROUPS = 1024;      // group maxima
 
@@ -44,21 +47,27 @@ constexpr uint32_t KEY_NEG_INF = 0x007fffffu;
 
 __device__ inline uint64_t entry_of(float v, int j) { return uint64_t(key_of(v)) << 32 | uint32_t(~uint32_t(j)); }
 
+// how many of the lanes in `mask` lie below this one
+__device__ inline int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(mask), 0));
+}
+
+template <int NW>
 struct TopLds {
-  uint64_t list[LIST];
+  __align__(16) uint64_t list[LIST + 2];
   uint32_t rank[LIST];
-  Raw chunk[CHUNKS];
-  int chunk_no[CHUNKS];
+  Raw chunk[NW][CHUNKS];
+  int chunk_no[NW][CHUNKS];
   uint16_t group[GROUPS];
   int pivots[2][16];
-  float part[16];
-  int ipart[2][16];
-  int count, chunks;
+  float part[NW];
+  int ipart[2][NW];
+  int count, overflow;
 };
 
 // Appends the entries among this thread's elements that `take` names.
 template <class T, int TPB, class F>
-__device__ inline void gather(const T* row, int vocab, TopLds& s, F take) {
+__device__ inline void gather(const T* row, int vocab, TopLds<TPB / 64>& s, F take) {
 #pragma unroll 1
   for (int j = threadIdx.x; j < vocab; j += TPB) {
     const float v = to_f32(row[j]);
@@ -72,7 +81,7 @@ __device__ inline void gather(const T* row, int vocab, TopLds& s, F take) {
 // The exact search: the K-th largest key by its bits, then, among the
 // elements of that key, the index up to which they belong to the K.
 template <class T, int TPB>
-__device__ void search(const T* row, int vocab, int k, TopLds& s) {
+__device__ void search(const T* row, int vocab, int k, TopLds<TPB / 64>& s) {
   auto count = [&](int flip, auto f) {
     int c = 0;
 #pragma unroll 1
@@ -106,20 +115,20 @@ __device__ void search(const T* row, int vocab, int k, TopLds& s) {
   __syncthreads();
 }
 
-template <class T, int CH, int TPB>
-__global__ __launch_bounds__(TPB, min_waves(CH)) void top_logits_kernel(const T* __restrict__ logits, int64_t n, int vocab,
+template <class T, class V>
+__global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* __restrict__ logits, int64_t n, int vocab,
                                                          int64_t ld, int k, float inv_t,
                                                          float* __restrict__ values,
                                                          int32_t* __restrict__ index,
                                                          float* __restrict__ lse) {
+  constexpr int CH = V::CH, TPB = V::TPB;
   constexpr int GP = GROUPS / TPB;  // groups of a thread
   constexpr int NW = TPB / 64;
-  __shared__ TopLds s;
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  __shared__ TopLds<NW> s;
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int full = vocab / E<T>;
   const float c = inv_t * 1.44269504088896340736f;
-  Row<T, CH, TPB> r;
-  r.clear();
+  Row<T, V> r;
   r.load(logits + int64_t(blockIdx.x) * ld, full, vocab);
   for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
     const T* lr = logits + row * ld;
@@ -129,28 +138,33 @@ __global__ __launch_bounds__(TPB, min_waves(CH)) void top_logits_kernel(const T*
     // ---- the largest of each group
     float g[GP];
     for (int i = 0; i < GP; ++i) g[i] = -__builtin_inff();
-    r.each(lr, full, [&](int i, int, const float(&x)[E<T>], const Raw&) {
+    r.each(lr, full, [&](int i, int, const float(&x)[E<T>], Raw) {
       const float top = max_of(x);
       g[i % GP] = max3(g[i % GP], top, top);
     });
     g[0] = max3(g[0], r.tail, r.tail);
-    float m = g[0];
-    for (int i = 1; i < GP; ++i) m = max3(m, g[i], g[i]);
-    for (int i = 0; i < GP; ++i) s.group[i * TPB + t] = uint16_t(key_of(g[i]) >> 16);
-    if (t == 0) s.count = 0, s.chunks = 0;
+    float mine = g[0];
+    for (int i = 1; i < GP; ++i) mine = max3(mine, g[i], g[i]);
+    if (k <= TPB / 4)
+      s.group[t] = uint16_t(key_of(mine) >> 16);
+    else
+      for (int i = 0; i < GP; ++i) s.group[i * TPB + t] = uint16_t(key_of(g[i]) >> 16);
+    if (t == 0) s.count = 0, s.overflow = 0;
+    float m = max3(mine, LOWEST, LOWEST);
     m = block_reduce<TPB>(m, s.part, Max());
     // ---- the K-th largest of them, from the top in steps of 4 bits
     uint32_t key = 0;
-    {
-      uint32_t v[GROUPS / 64];
-      for (int i = 0; i < GROUPS / 64; ++i) v[i] = s.group[i * 64 + lane];
+    auto kth = [&](auto per_lane) {
+      constexpr int G = decltype(per_lane)::value;
+      uint32_t v[G];
+      for (int i = 0; i < G; ++i) v[i] = s.group[i * 64 + lane];
 #pragma unroll 1
       for (int step = 0; step < 4; ++step) {
 #pragma unroll 1
         for (int p = w; p < 16; p += NW) {
           const uint32_t pivot = key + (uint32_t(p) << (12 - 4 * step));
           int cnt = 0;
-          for (int i = 0; i < GROUPS / 64; ++i) cnt += __popcll(__ballot(v[i] >= pivot));
+          for (int i = 0; i < G; ++i) cnt += __popcll(__ballot(v[i] >= pivot));
           if (lane == 0) s.pivots[step & 1][p] = cnt;
         }
         __syncthreads();
@@ -158,47 +172,58 @@ __global__ __launch_bounds__(TPB, min_waves(CH)) void top_logits_kernel(const T*
         for (int p = 1; p < 16; ++p) best = s.pivots[step & 1][p] >= k ? p : best;
         key += uint32_t(best) << (12 - 4 * step);
       }
-    }
+    };
+    // a group for each thread will do for lists of up to a quarter as many
+    if (k <= TPB / 4) kth(std::integral_constant<int, TPB / 64>());
+    else kth(std::integral_constant<int, GROUPS / 64>());
     // too few groups reach above -inf: so does tau
     const float tau = key <= (KEY_NEG_INF >> 16) ? -__builtin_inff() : value_of(key << 16);
     // ---- candidates, and the sum of exponentials
-    const float ref = m == -__builtin_inff() ? 0.f : m;
     float sum = 0.f;
-    auto append = [&](float v, int j) {
-      const int at = atomicAdd(&s.count, 1);
-      if (at < LIST) s.list[at] = entry_of(v, j);
-    };
-    r.each(lr, full, [&](int i, int ch, const float(&x)[E<T>], const Raw& q) {
-      if (max_of(x) >= tau && ch < full) {
-        const int at = atomicAdd(&s.chunks, 1);
-        if (at < CHUNKS) s.chunk[at] = q, s.chunk_no[at] = ch;
+    int held = 0;  // of this wave's chunks, in LDS
+    r.template each<true>(lr, full, [&](int i, int ch, const float(&x)[E<T>], Raw q) {
+      const bool hit = max_of(x) >= tau && ch < full;
+      const uint64_t hits = __ballot(hit);
+      if (hits) {
+        const int at = held + lanes_below(hits);
+        if (hit && at < CHUNKS) s.chunk[w][at] = q, s.chunk_no[w][at] = ch;
+        held += __popcll(hits);
       }
       float part = 0.f;
-      for (int e = 0; e < E<T>; ++e) part += __builtin_amdgcn_exp2f((x[e] - ref) * c);
+      for (int e = 0; e < E<T>; ++e) part += __builtin_amdgcn_exp2f((x[e] - m) * c);
       sum += part;
       // computed here, not where the sum is used: the elements would be kept
       asm volatile("" : "+v"(sum));
-      if constexpr (CH > 0)
-        r.load_chunk(i, nr, ahead);
+      if constexpr (CH > 0) r.load_chunk(i, nr, ahead);
     });
-    if (r.tail >= tau && full * E<T> + t < vocab) append(r.tail, full * E<T> + t);
-    sum += __builtin_amdgcn_exp2f((r.tail - ref) * c);
+    // the elements of the wave's chunks, and the tail, at or above tau
+    auto append = [&](bool take, float v, int j) {
+      const uint64_t takes = __ballot(take);
+      if (!takes) return;
+      int base = 0;
+      if (lane == 0) base = atomicAdd(&s.count, __popcll(takes));
+      const int at = __builtin_amdgcn_readfirstlane(base) + lanes_below(takes);
+      if (take && at < LIST) s.list[at] = entry_of(v, j);
+    };
+    append(r.tail >= tau && full * E<T> + t < vocab, r.tail, full * E<T> + t);
+    sum += __builtin_amdgcn_exp2f((r.tail - m) * c);
     if (more) r.load_tail(nr, full, vocab);
-    sum = block_reduce<TPB>(sum, s.part, Sum());
-    const int chunks = s.chunks;
+    if (held > CHUNKS) s.overflow = 1;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int items = min(held, CHUNKS) * E<T>;
 #pragma unroll 1
-    for (int i = t; i < (chunks < CHUNKS ? chunks : CHUNKS) * E<T>; i += TPB) {
-      const Raw q = s.chunk[i / E<T>];
-      float x[E<T>];
-      unpack(q, x);
-      float v = x[0];
-      for (int e = 1; e < E<T>; ++e) v = i % E<T> == e ? x[e] : v;
-      if (v >= tau) append(v, s.chunk_no[i / E<T>] * E<T> + i % E<T>);
+    for (int i = lane; i - lane < items; i += 64) {
+      const int at = min(i, items - 1) / E<T>, e = i % E<T>;
+      const uint32_t word = reinterpret_cast<const uint32_t*>(&s.chunk[w][at])[E<T> == 8 ? e / 2 : e];
+      const float v = __uint_as_float(E<T> == 4 ? word : e & 1 ? word & 0xffff0000u : word << 16);
+      append(i < items && v >= tau, v, s.chunk_no[w][at] * E<T> + e);
     }
-    __syncthreads();
-    if (lse && t == 0) lse[row] = ref * inv_t + logf(sum);
+    sum = block_reduce<TPB>(sum, s.part, Sum());
+    // (no finite logit: the sum is 0)
+    if (lse && t == 0) lse[row] = sum == 0.f ? -__builtin_inff() : m * inv_t + logf(sum);
     int count = s.count;
-    if (chunks > CHUNKS || count > LIST || sum != sum) {
+    if (s.overflow || count > LIST || sum != sum) {
       __syncthreads();
       if (t == 0) s.count = 0;
       __syncthreads();
@@ -215,12 +240,17 @@ __global__ __launch_bounds__(TPB, min_waves(CH)) void top_logits_kernel(const T*
     while (width < count && width < TPB) width *= 2;
 #pragma unroll 1
     for (int i = t; i < count; i += TPB) s.rank[i] = 0;
+    if (t == 0) s.list[count] = 0;  // (below every entry: the list is read in pairs)
     __syncthreads();
 #pragma unroll 1
     for (int i = t & (width - 1); i < count; i += width) {
       const uint64_t mine = s.list[i];
       uint32_t before = 0;
-      for (int j = t / width; j < count; j += TPB / width) before += s.list[j] > mine;
+#pragma unroll 4
+      for (int j = 2 * (t / width); j < count; j += 2 * (TPB / width)) {
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(s.list + j);
+        before += (two.x > mine) + (two.y > mine);
+      }
       if (before) atomicAdd(&s.rank[i], before);
     }
     __syncthreads();
@@ -242,15 +272,27 @@ int32_t logits_max_k() { return K_MAX; }
 
 kq_status top_logits_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld, int k,
                          float temperature, float* values, int32_t* index, float* lse, hipStream_t s) {
-  auto launch = [&](auto* p) {
+  auto launch = [&](auto* p) -> kq_status {
     using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
-    return with_variant(cdiv(vocab, E<T>), [&](auto v) -> kq_status {
+    const int64_t chunks = cdiv(vocab, E<T>);
+    auto go = [&](auto v) -> kq_status {
       using V = decltype(v);
-      top_logits_kernel<T, V::CH, V::TPB><<<row_groups<V>(n), V::TPB, 0, s>>>(
-          p, n, int(vocab), ld, k, 1.f / temperature, values, index, lse);
+      top_logits_kernel<T, V><<<row_groups<V>(n), V::TPB, 0, s>>>(p, n, int(vocab), ld, k, 1.f / temperature,
+                                                                  values, index, lse);
       KQ_HIP(hipGetLastError());
       return KQ_OK;
-    });
+    };
+    // Held in registers, in workgroups as small as take the row in 16 chunks
+    // a thread (4096 x 32000 bf16: 74 us with 256 threads, 90 with 512), and
+    // of the largest rows those that fit at all (4096 x 128256 bf16: 251 us,
+    // read twice 311). The number of rows has no say, so that a row's sum,
+    // and its rounding, is the same in whatever company.
+    if (chunks <= 1024) return go(Variant<4, 256, 6>());
+    if (chunks <= 2048) return go(Variant<8, 256, 5>());
+    if (chunks <= 4096) return go(Variant<16, 256, 4>());
+    if (chunks <= 8192) return go(Variant<16, 512, 4>());
+    if (chunks <= 16384) return go(Variant<32, 512, 2>());
+    return go(Variant<0, 512, 6>());
   };
   if (dt == KQ_BF16) return launch(static_cast<const uint16_t*>(logits));
   return launch(static_cast<const float*>(logits));
