@@ -260,14 +260,15 @@ kq_status distill_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab,
       return go(Variant<0, 1024, 8>(), no, yes);
     }
     // Loss and gradient: two passes. Rows of up to 128 KB are held in
-    // registers (4096 x 32000 bf16: 119 us, read twice 126; 4096 x 65536: 239,
-    // 256); of longer ones a CU holds too few at once to keep the memory
+    // registers (4096 x 32000 bf16: 115 us, read twice 126; 4096 x 65536: 220,
+    // 234); of longer ones a CU holds too few at once to keep the memory
     // busy, and the second pass finds them in the cache beside it (4096 x
-    // 128256: 467 us, in registers 581).
+    // 128256: 463 us, in registers 531 to 599).
     if (chunks <= 512) return go(Variant<2, 256, 6>(), yes, yes);
     if (chunks <= 1024) return go(Variant<4, 256, 6>(), yes, yes);
     if (chunks <= 2048) return go(Variant<8, 256, 5>(), yes, yes);
     if (chunks <= 4096) return go(Variant<16, 256, 4>(), yes, yes);
+    if (chunks <= 6144) return go(Variant<24, 256, 3>(), yes, yes);
     if (chunks <= 8192) return go(Variant<16, 512, 4>(), yes, yes);
     return go(Variant<0, 512, 6>(), yes, yes);
   };
