@@ -403,7 +403,7 @@ _DT = {torch.bfloat16: N.KQ_BF16, torch.float32: N.KQ_F32}
 
 
 def _raw_stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=1024)
@@ -557,11 +557,12 @@ def kq_linear_i8(x, w, w_scale, w_zero=None, bias=None, clip: float = 1.0, y=Non
     f32 = torch.float32
     y, ldy = _product_out(y, n, d_out, dtype or x.dtype, dev, stream)
     if ws is None:
-        ws = _empty((_need(N.KQ_OP_LINEAR_I8, d_out, d_in, n),), torch.uint8, dev, stream)
+        need = _need(N.KQ_OP_LINEAR_I8, d_out, d_in, n)
+        ws = _empty((need,), torch.uint8, dev, stream) if need else None
     check(N.lib.kq_linear_i8(x.data_ptr(), _DT[x.dtype], ldx, clip, pw, _flat(w_scale, d_out, f32, "w_scale"),
                              _flat(w_zero, d_out, f32, "w_zero"), _flat(bias, d_out, f32, "bias"), n, d_out,
-                             d_in, y.data_ptr(), _DT[y.dtype], ldy, ws.data_ptr(), _nbytes(ws),
-                             _raw_stream(stream, dev)))
+                             d_in, y.data_ptr(), _DT[y.dtype], ldy, None if ws is None else ws.data_ptr(),
+                             0 if ws is None else _nbytes(ws), _raw_stream(stream, dev)))
     return y
 
 

@@ -10,6 +10,7 @@
 //
 // Code rows (tokens and channels alike) are padded with zeros to a multiple of
 // 128 bytes, so the products read whole rows without a tail.
+#include <algorithm>
 #include <type_traits>
 
 #include "kq_internal.h"
@@ -46,10 +47,57 @@ struct __attribute__((packed, aligned(2))) Raw16 {
   uint32_t w[4];
 };
 
-// the code of one value; s > 0 and finite
-__device__ inline int i8_code(float v, float s) {
-  return int(fminf(fmaxf(rintf(v / s), -127.f), 127.f));
+// What a row's codes are made with. rint(v / s) asks for the correctly rounded
+// quotient; v * (1 / s) is off from it by at most 127 * 2^-22 = 3e-5, so where it
+// lies further than 1e-4 from a midpoint between two codes, both round to
+// the same one, and the division (10 operations) is left for the few others.
+struct I8Grid {
+  float s, inv;  // s NaN or 0: all codes are 0
+
+  __device__ explicit I8Grid(float scale) : s(scale), inv(scale >= 1e-37f ? 1.f / scale : 0.f) {}
+  __device__ int code(float v) const {
+    const float t = v * inv;
+    float q = rintf(t);
+    // (no reciprocal of a scale near the smallest numbers, or NaN)
+    if (inv == 0.f || fabsf(fabsf(t - q) - 0.5f) < 1e-4f) q = s > 0.f ? rintf(v / s) : 0.f;
+    return int(fminf(fmaxf(q, -127.f), 127.f));
+  }
+};
+
+// scale of a row whose largest magnitude has the bits m: NaN if the row has an
+// infinity or a NaN (they order above the numbers)
+__device__ inline float i8_scale(uint32_t m, float clip) {
+  return m >= 0x7f800000u ? __builtin_nanf("") : clip * __uint_as_float(m) / 127.f;
 }
+
+// 16 bytes of a row: the largest magnitude's bits so far, and the codes
+template <class T>
+struct I8Chunk {
+  static constexpr int E = 16 / int(sizeof(T));
+  static __device__ inline uint32_t largest(uint32_t m, const Raw16& q) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // (the upper half of a pair of bfloat16 is compared with the lower one
+      // behind it, which own() takes away)
+      m = max(m, q.w[k] & 0x7fffffffu);
+      if (E == 8) m = max(m, (q.w[k] << 16) & 0x7fffffffu);
+    }
+    return m;
+  }
+  static __device__ inline uint32_t own(uint32_t m) { return E == 8 ? m & 0xffff0000u : m; }
+  // codes of the elements, and their sum added to `sum`
+  static __device__ inline void codes(const Raw16& q, const I8Grid& g, uint32_t (&out)[E / 4], int& sum) {
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) out[k] = 0;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const uint32_t u = q.w[E == 8 ? k / 2 : k];
+      const int c = g.code(__uint_as_float(E == 4 ? u : k & 1 ? u & 0xffff0000u : u << 16));
+      sum += c;
+      out[k / 4] |= uint32_t(c & 255) << (8 * (k % 4));
+    }
+  }
+};
 
 // A row in registers: CH chunks of 16 bytes a thread, read once (chunk c is
 // register c / TPB of thread c % TPB), rounded and written as 16-byte (fp32:
@@ -63,7 +111,8 @@ __global__ __launch_bounds__(TPB) void quantize_rows_kernel(const T* __restrict_
                                                             int8_t* __restrict__ codes,
                                                             float* __restrict__ scale,
                                                             int32_t* __restrict__ sums) {
-  constexpr int E = 16 / int(sizeof(T)), NW = TPB / 64;
+  using Chunk = I8Chunk<T>;
+  constexpr int E = Chunk::E, NW = TPB / 64;
   __shared__ uint32_t pm[NW];
   __shared__ int ps[NW];
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
@@ -71,8 +120,6 @@ __global__ __launch_bounds__(TPB) void quantize_rows_kernel(const T* __restrict_
   const T* xr = x + row * ldx;
   const int full = d / E;
   Raw16 q[CH];
-  // magnitudes order as integers, an infinity and every NaN above the rest
-  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     q[i] = Raw16{};
@@ -80,46 +127,32 @@ __global__ __launch_bounds__(TPB) void quantize_rows_kernel(const T* __restrict_
   }
   float tail = 0.f;
   if (full * E + t < d) tail = load_f32(xr + full * E + t);
+  uint32_t m = __float_as_uint(fabsf(tail));
 #pragma unroll
-  for (int i = 0; i < CH; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t u = q[i].w[k];
-      m = max(m, u & 0x7fffffffu);
-      if (E == 8) m = max(m, (u << 16) & 0x7fffffffu);
-    }
-  // (the upper half of a pair carries the lower one's bits: a bfloat16's own
-  // are cut out below)
-  m = max(m, __float_as_uint(fabsf(tail)));
-  if (E == 8) m &= 0xffff0000u;
+  for (int i = 0; i < CH; ++i) m = Chunk::largest(m, q[i]);
+  m = Chunk::own(m);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(m, o)));
   if (lane == 0) pm[w] = m;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < NW; ++k) m = max(m, pm[k]);
-  const float s = m >= 0x7f800000u ? __builtin_nanf("") : clip * __uint_as_float(m) / 127.f;
+  const float s = i8_scale(m, clip);
+  const I8Grid grid(s);
   int8_t* cr = codes + row * row_bytes;
   int sum = 0;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = i * TPB + t;
     if (c < full) {
-      uint32_t out[E / 4] = {};
-#pragma unroll
-      for (int k = 0; k < E; ++k) {
-        const uint32_t u = q[i].w[E == 8 ? k / 2 : k];
-        const float v = __uint_as_float(E == 4 ? u : k & 1 ? u & 0xffff0000u : u << 16);
-        const int code = s > 0.f ? i8_code(v, s) : 0;
-        sum += code;
-        out[k / 4] |= uint32_t(code & 255) << (8 * (k % 4));
-      }
+      uint32_t out[E / 4];
+      Chunk::codes(q[i], grid, out, sum);
       __builtin_memcpy(__builtin_assume_aligned(cr + c * E, E), out, E);
     }
   }
   // the last elements, and the zeros up to the row's end
   for (int k = full * E + t; k < row_bytes; k += TPB) {
-    const int code = k < d && s > 0.f ? i8_code(tail, s) : 0;
+    const int code = k < d ? grid.code(tail) : 0;
     sum += code;
     cr[k] = int8_t(code);
   }
@@ -146,6 +179,8 @@ __global__ __launch_bounds__(256) void pack_i8_kernel(const uint8_t* __restrict_
   if (threadIdx.x == 0) zero_out[row] = zero[row] - 128.f;
 }
 
+// y of one sum (see the top of the file): the conversion of the exact sum, the
+// two scales and the bias each round once
 struct I8Epi {
   const float* a_scale;
   const int32_t* a_sum;
@@ -153,6 +188,13 @@ struct I8Epi {
   const float* w_zero;  // NULL: symmetric
   const float* bias;    // NULL: none
   int64_t n, m, ldy;
+
+  template <class Y>
+  __device__ __forceinline__ void put(int sum, int64_t t, int64_t o, Y* y) const {
+    if (w_zero) sum -= int(rintf(w_zero[o])) * a_sum[t];
+    const float f = float(sum) * a_scale[t] * w_scale[o];
+    store_y(y + t * ldy + o, bias ? f + bias[o] : f);
+  }
 };
 
 // ---------------------------------------------------------------- the GEMM
@@ -209,7 +251,7 @@ struct I8Tile {
 // bias each round once; y is rounded to its type after that.
 template <int MI, int NJ, class Y>
 __device__ inline void i8_store(const v16i (&acc)[MI][NJ], const I8Epi& e, int64_t t0, int64_t o0,
-                                char* slab, Y* y) {
+                                char* slab, Y* y, int32_t* partial) {
   constexpr int W = 32 * MI;                              // channels of a wave
   constexpr int ROWB = W * 4 + 16;                        // padded: rows start in other banks
   constexpr int CH = 16 / int(sizeof(Y));                 // channels of a lane: 16 bytes of y
@@ -239,9 +281,16 @@ __device__ inline void i8_store(const v16i (&acc)[MI][NJ], const I8Epi& e, int64
       const int row = p * (64 / LPR) + lane / LPR;
       const int64_t tk = t0 + 32 * j + row;
       if (tk < e.n) {
+        const v4i* src = reinterpret_cast<const v4i*>(slab + row * ROWB + lane % LPR * CH * 4);
+        if (partial) {  // a share of K: the sums as they are
+          int32_t* dst = partial + tk * e.m + o;
+#pragma unroll
+          for (int k = 0; k < CH; ++k)
+            if (o + k < e.m) dst[k] = src[k / 4][k % 4];
+          continue;
+        }
         const float as = e.a_scale[tk];
         const int32_t sum = e.w_zero ? e.a_sum[tk] : 0;
-        const v4i* src = reinterpret_cast<const v4i*>(slab + row * ROWB + lane % LPR * CH * 4);
         Y v[CH];
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
@@ -280,18 +329,20 @@ __device__ inline bool i8_tile(int nt, int no, int* ti, int* oi) {
 template <class C, class Y>
 __global__ __launch_bounds__(64 * C::NW) void gemm_i8_kernel(const int8_t* __restrict__ a,
                                                              const int8_t* __restrict__ w, int64_t rb, I8Epi e,
-                                                             Y* __restrict__ y) {
+                                                             Y* __restrict__ y, int32_t* __restrict__ partial) {
   constexpr int TM = C::TM, TN = C::TN, KB = C::KB, KS = KB / 32;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int ti, oi;
   if (!i8_tile(int(cdiv(e.n, TM)), int(cdiv(e.m, TN)), &ti, &oi)) return;
   const int64_t t0 = int64_t(ti) * TM, o0 = int64_t(oi) * TN;
-  const int stages = int(rb / KB);
+  // this share of the stages of K (of gridDim.y)
+  const int all = int(rb / KB), s0 = int(int64_t(all) * blockIdx.y / gridDim.y);
+  const int stages = int(int64_t(all) * (blockIdx.y + 1) / gridDim.y) - s0;
   // rows of a stage: TN channels, then TM tokens (the last one again where
   // the matrix ends)
-  const int8_t* wb = w + o0 * rb;
-  const int8_t* ab = a + t0 * rb;
+  const int8_t* wb = w + o0 * rb + int64_t(s0) * KB;
+  const int8_t* ab = a + t0 * rb + int64_t(s0) * KB;
   uint32_t off[C::PER];
 #pragma unroll
   for (int j = 0; j < C::PER; ++j) {
@@ -391,33 +442,66 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_i8_kernel(const int8_t* __res
   }
   __syncthreads();
   i8_store<C::MI, C::NJ>(acc, e, t0 + (wv / C::WO) * (TM / C::WT), o0 + (wv % C::WO) * (TN / C::WO),
-                         lds + wv * C::SLAB, y);
+                         lds + wv * C::SLAB, y,
+                         gridDim.y > 1 ? partial + int64_t(blockIdx.y) * e.n * e.m : nullptr);
 }
 
 template <class C, class Y>
-kq_status gemm_i8_launch(const int8_t* a, const int8_t* w, int64_t rb, const I8Epi& e, Y* y, hipStream_t s) {
+kq_status gemm_i8_launch(const int8_t* a, const int8_t* w, int64_t rb, const I8Epi& e, Y* y, int splits,
+                         int32_t* partial, hipStream_t s) {
   const auto kernel = gemm_i8_kernel<C, Y>;
   KQ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                              C::LDS));
-  kernel<<<unsigned(8 * cdiv(cdiv(e.n, C::TM) * cdiv(e.m, C::TN), 8)), 64 * C::NW, C::LDS, s>>>(a, w, rb, e, y);
+  const dim3 grid(unsigned(8 * cdiv(cdiv(e.n, C::TM) * cdiv(e.m, C::TN), 8)), unsigned(splits));
+  kernel<<<grid, 64 * C::NW, C::LDS, s>>>(a, w, rb, e, y, partial);
   KQ_HIP(hipGetLastError());
   return KQ_OK;
 }
 
 // ------------------------------------------------------- few tokens
-// The codes of 16 RT channels stream from memory through the registers of 16
+// The codes of 16 RT channels stream from memory through the registers of SW
 // waves, which take the row's 128-byte lines in turn, and meet the codes of
 // 16 TT tokens (from L2) in v_mfma_i32_16x16x64_i8 (A: channels, B: tokens;
 // lane l holds 16 bytes of row l % 16 at k = 16 (l / 16), and of the result
 // channels 4 (l / 16) + r of token l % 16 in register r). The waves' sums
 // are joined in LDS: integers, in any order the same.
-constexpr int SW = 16;  // waves of a workgroup
+template <int RT, int TT, int SW>
+struct StreamTile {
+  v4i acc[RT][TT];
 
-template <int RT, int TT, class Y>
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[r][t] = v4i{0, 0, 0, 0};
+  }
+  // The sums of the workgroup's waves, joined: finish(sum, channel, token) for
+  // each, by one thread. part: SW * RT * TT * 64 vectors of LDS.
+  template <class F>
+  __device__ __forceinline__ void join(v4i* part, int wv, int lane, F finish) const {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) part[(wv * RT * TT + r * TT + t) * 64 + lane] = acc[r][t];
+    __syncthreads();
+    for (int j = threadIdx.x; j < RT * TT * 256; j += 64 * SW) {
+      const int c = j % (16 * RT), tk = j / (16 * RT);
+      const int tile = (c / 16) * TT + tk / 16, ln = (c % 16 / 4) * 16 + tk % 16;
+      int sum = 0;
+#pragma unroll
+      for (int k = 0; k < SW; ++k) sum += part[(k * RT * TT + tile) * 64 + ln][c % 4];
+      finish(sum, c, tk);
+    }
+  }
+};
+
+// gridDim.y workgroups share the lines of a row of codes; with more than one,
+// their sums go to `partial` (gridDim.y x n x m) and are joined afterwards.
+template <int RT, int TT, int SW, class Y>
 __global__ __launch_bounds__(64 * SW) void stream_i8_kernel(const int8_t* __restrict__ a,
                                                             const int8_t* __restrict__ w, int64_t rb, I8Epi e,
-                                                            Y* __restrict__ y) {
-  __shared__ v4i part[SW][RT * TT][64];
+                                                            Y* __restrict__ y, int32_t* __restrict__ partial) {
+  __shared__ v4i part[SW * RT * TT * 64];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
   const int64_t o0 = int64_t(blockIdx.x) * (16 * RT);
   const int8_t *wp[RT], *ap[TT];
@@ -425,21 +509,18 @@ __global__ __launch_bounds__(64 * SW) void stream_i8_kernel(const int8_t* __rest
   for (int r = 0; r < RT; ++r) wp[r] = w + min(o0 + 16 * r + i, e.m - 1) * rb + 16 * g;
 #pragma unroll
   for (int t = 0; t < TT; ++t) ap[t] = a + min(int64_t(16 * t + i), e.n - 1) * rb + 16 * g;
-  v4i acc[RT][TT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[r][t] = v4i{0, 0, 0, 0};
+  StreamTile<RT, TT, SW> tile;
+  tile.clear();
   constexpr int U = TT == 1 ? 4 : 2;  // 128-byte lines in flight
-  const int lines = int(rb / 128);
-  auto step = [&](int line, auto count) {
+  const int lines = int(rb / 128), step = SW * int(gridDim.y);
+  auto run = [&](int line, auto count) {
     constexpr int N = decltype(count)::value;
     v4i fw[N][2][RT], fa[N][2][TT];
 #pragma unroll
     for (int u = 0; u < N; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t k = int64_t(line + u * SW) * 128 + 64 * h;
+        const int64_t k = int64_t(line + u * step) * 128 + 64 * h;
 #pragma unroll
         for (int r = 0; r < RT; ++r) fw[u][h][r] = *reinterpret_cast<const v4i*>(wp[r] + k);
 #pragma unroll
@@ -453,34 +534,144 @@ __global__ __launch_bounds__(64 * SW) void stream_i8_kernel(const int8_t* __rest
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int t = 0; t < TT; ++t)
-            acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][h][r], fa[u][h][t], acc[r][t], 0, 0, 0);
+            tile.acc[r][t] =
+                __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][h][r], fa[u][h][t], tile.acc[r][t], 0, 0, 0);
   };
-  int line = wv;
-  for (; line + (U - 1) * SW < lines; line += U * SW) step(line, std::integral_constant<int, U>());
-  for (; line < lines; line += SW) step(line, std::integral_constant<int, 1>());
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) part[wv][r * TT + t][lane] = acc[r][t];
-  __syncthreads();
-  // one sum a thread: channel c of token tk
-  for (int j = threadIdx.x; j < RT * TT * 256; j += 64 * SW) {
-    const int c = j % (16 * RT), tk = j / (16 * RT);
+  int line = int(blockIdx.y) * SW + wv;
+  for (; line + (U - 1) * step < lines; line += U * step) run(line, std::integral_constant<int, U>());
+  for (; line < lines; line += step) run(line, std::integral_constant<int, 1>());
+  tile.join(part, wv, lane, [&](int sum, int c, int tk) {
     const int64_t o = o0 + c;
-    if (tk >= e.n || o >= e.m) continue;
-    const int tile = (c / 16) * TT + tk / 16, ln = (c % 16 / 4) * 16 + tk % 16;
-    int sum = 0;
-#pragma unroll
-    for (int k = 0; k < SW; ++k) sum += part[k][tile][ln][c % 4];
-    if (e.w_zero) sum -= int(rintf(e.w_zero[o])) * e.a_sum[tk];
-    const float f = float(sum) * e.a_scale[tk] * e.w_scale[o];
-    store_y(y + tk * e.ldy + o, e.bias ? f + e.bias[o] : f);
-  }
+    if (tk >= e.n || o >= e.m) return;
+    if (gridDim.y > 1) partial[(int64_t(blockIdx.y) * e.n + tk) * e.m + o] = sum;
+    else e.put(sum, tk, o, y);
+  });
 }
 
-template <int RT, int TT, class Y>
-kq_status stream_i8_launch(const int8_t* a, const int8_t* w, int64_t rb, const I8Epi& e, Y* y, hipStream_t s) {
-  stream_i8_kernel<RT, TT><<<unsigned(cdiv(e.m, 16 * RT)), 64 * SW, 0, s>>>(a, w, rb, e, y);
+// The smallest calls: the same with the tokens rounded on the way, by every
+// workgroup for itself (into LDS, rows 16 bytes apart from a multiple of 128
+// so that 16 tokens' chunks lie in different banks). The waves split the
+// tokens among them; the first weights are on their way meanwhile.
+constexpr int FUSED_CH(int size) { return size == 2 ? 4 : 8; }  // chunks of a thread
+// waves for a token
+__host__ __device__ constexpr int fused_waves(int64_t n) { return n <= 1 ? 16 : n <= 2 ? 8 : n <= 4 ? 4 : n <= 8 ? 2 : 1; }
+
+template <class T, class Y>
+__global__ __launch_bounds__(1024) void fused_i8_kernel(const T* __restrict__ x, int d, int64_t ldx,
+                                                           float clip, const int8_t* __restrict__ w, int64_t rb,
+                                                           I8Epi e, Y* __restrict__ y) {
+  using Chunk = I8Chunk<T>;
+  constexpr int E = Chunk::E, CH = FUSED_CH(sizeof(T)), U = 2, SW = 16;
+  extern __shared__ __attribute__((aligned(16))) int8_t codes[];
+  __shared__ v4i part[SW * 64];
+  __shared__ uint32_t pm[SW];
+  __shared__ int ps[SW];
+  __shared__ float scale[16];
+  __shared__ int sums[16];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int64_t o0 = int64_t(blockIdx.x) * 16;
+  const int lines = int(rb / 128), rs = int(rb) + 16;
+  const int8_t* wp = w + min(o0 + i, e.m - 1) * rb + 16 * g;
+  v4i first[U][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      first[u][h] = *reinterpret_cast<const v4i*>(wp + int64_t(min(wv + u * SW, lines - 1)) * 128 + 64 * h);
+  // ---- the tokens: wave wv takes part of token wv / wpt
+  const int wpt = fused_waves(e.n), tok = wv / wpt, at = (wv % wpt) * 64 + lane, step = 64 * wpt;
+  const bool have = tok < e.n;
+  const T* xr = x + (have ? tok : 0) * ldx;
+  const int full = d / E;
+  Raw16 q[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    q[k] = Raw16{};
+    if (have && at + k * step < full) q[k] = *reinterpret_cast<const Raw16*>(xr + int64_t(at + k * step) * E);
+  }
+  float tail = 0.f;
+  if (have && full * E + at < d) tail = load_f32(xr + full * E + at);
+  uint32_t m = __float_as_uint(fabsf(tail));
+#pragma unroll
+  for (int k = 0; k < CH; ++k) m = Chunk::largest(m, q[k]);
+  m = Chunk::own(m);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(m, o)));
+  if (lane == 0) pm[wv] = m;
+  __syncthreads();
+  for (int k = 0; k < wpt; ++k) m = max(m, pm[tok * wpt + k]);
+  const float s = i8_scale(m, clip);
+  const I8Grid grid(s);
+  int8_t* cr = codes + tok * rs;
+  int sum = 0;
+  if (have) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = at + k * step;
+      if (c < full) {
+        uint32_t out[E / 4];
+        Chunk::codes(q[k], grid, out, sum);
+        __builtin_memcpy(__builtin_assume_aligned(cr + c * E, E), out, E);
+      }
+    }
+    for (int k = full * E + at; k < rb; k += step) {
+      const int code = k < d ? grid.code(tail) : 0;
+      sum += code;
+      cr[k] = int8_t(code);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  if (lane == 0) ps[wv] = sum;
+  __syncthreads();
+  if (threadIdx.x < e.n) {
+    int total = 0;
+    for (int k = 0; k < wpt; ++k) total += ps[threadIdx.x * wpt + k];
+    sums[threadIdx.x] = total;
+  }
+  if (have && at == 0) scale[tok] = s;
+  // ---- the product
+  const int8_t* ap = codes + min(i, int(e.n) - 1) * rs + 16 * g;
+  StreamTile<1, 1, SW> tile;
+  tile.clear();
+  auto mma = [&](const v4i& fw, int line, int h) {
+    const v4i fa = *reinterpret_cast<const v4i*>(ap + line * 128 + 64 * h);
+    tile.acc[0][0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw, fa, tile.acc[0][0], 0, 0, 0);
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (wv + u * SW < lines) mma(first[u][h], wv + u * SW, h);
+#pragma unroll 2
+  for (int line = wv + U * SW; line < lines; line += SW) {
+    const v4i f0 = *reinterpret_cast<const v4i*>(wp + int64_t(line) * 128);
+    const v4i f1 = *reinterpret_cast<const v4i*>(wp + int64_t(line) * 128 + 64);
+    mma(f0, line, 0);
+    mma(f1, line, 1);
+  }
+  e.a_scale = scale;
+  e.a_sum = sums;
+  tile.join(part, wv, lane, [&](int acc, int c, int tk) {
+    if (tk < e.n && o0 + c < e.m) e.put(acc, tk, o0 + c, y);
+  });
+}
+
+// y from the sums that `splits` workgroups left
+template <class Y>
+__global__ __launch_bounds__(256) void join_i8_kernel(const int32_t* __restrict__ partial, int splits, I8Epi e,
+                                                      Y* __restrict__ y) {
+  const int64_t per = cdiv(e.m, 256), t = blockIdx.x / per;
+  const int64_t o = (blockIdx.x - t * per) * 256 + threadIdx.x;
+  if (o >= e.m) return;
+  int sum = 0;
+  for (int k = 0; k < splits; ++k) sum += partial[(int64_t(k) * e.n + t) * e.m + o];
+  e.put(sum, t, o, y);
+}
+
+template <class Y>
+kq_status join_i8_launch(const int32_t* partial, int splits, const I8Epi& e, Y* y, hipStream_t s) {
+  join_i8_kernel<<<unsigned(cdiv(e.m, 256) * e.n), 256, 0, s>>>(partial, splits, e, y);
   KQ_HIP(hipGetLastError());
   return KQ_OK;
 }
@@ -518,37 +709,111 @@ kq_status pack_i8_run(const uint8_t* codes, const float* zero, int64_t d_out, in
   return KQ_OK;
 }
 
-size_t matmul_i8_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
+namespace {
+
+// How a product is taken, by its sizes alone.
+enum I8Kind { I8_STREAM, I8_64, I8_128, I8_128_256, I8_256 };
+struct I8Plan {
+  I8Kind kind;
+  int rt;      // streams: 16-channel tiles of a workgroup
+  int splits;  // shares of K
+};
+
+I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
+  const int64_t lines = cdiv(d, I8_PAD);
+  if (n <= 32) {
+    // Few tokens: the weights' bytes are what counts. Up to 16 tokens take 16
+    // channels a workgroup (1 token, 8192 -> 28672: 41 us, with 32 channels
+    // 72; 12 tokens, 28672 -> 8192: 58, with 32 channels 56); with more, the
+    // tokens' own bytes are read less often the more channels meet them, as
+    // long as every CU has a workgroup (32 tokens, 8192 -> 28672: 89 us with 16
+    // channels, 73 with 32, 59 with 64; 4096 -> 4096: 9, 11 and 17). Long rows
+    // of few channels are shared (16 tokens, 28672 -> 1024: 30 us, shared 16).
+    I8Plan p{I8_STREAM, n <= 16 || m < 8192 ? 1 : m < 16384 ? 2 : 4, 1};
+    const int64_t groups = cdiv(m, 16 * p.rt);
+    if (groups < 256 && lines >= 128) p.splits = int(std::min(cdiv(256, groups), lines / 64));
+    return p;
+  }
+  // The tile: the CU with most tiles takes k = ceil(tiles / 256) of them, each
+  // some time for every 128-byte stage of K and some at its ends. Fitted to
+  // 8192 tokens, 28672 -> 8192 (1562 us with 256 x 256, 1775, 1889 and 3241
+  // with 128 x 256, 128 x 128 and 64 x 64), 4096, 4096 -> 4096 (68, 83, 84,
+  // 126) and 512, 4096 -> 4096 (50, 32, 27, 17, where a CU has one of the small
+  // tiles for itself). With fewer tiles than CUs the stages are shared, for
+  // the launch that joins the sums and its traffic.
+  static const struct {
+    I8Kind kind;
+    int64_t tm, tn;
+    double stage, ends, lone_stage;
+  } tiles[] = {{I8_256, 256, 256, 1.705, 5.0, 1.705},
+               {I8_128_256, 128, 256, 0.949, 9.5, 0.949},
+               {I8_128, 128, 128, 0.509, 4.0, 0.86},
+               {I8_64, 64, 64, 0.223, 0.7, 0.27}};
+  I8Plan best{I8_64, 0, 1};
+  double least = 1e30;
+  for (const auto& t : tiles) {
+    const int64_t count = cdiv(n, t.tm) * cdiv(m, t.tn);
+    for (int64_t splits = 1; splits <= 8; splits *= 2) {
+      if (splits > 1 && (count * splits > 512 || lines < 4 * splits)) break;
+      const int64_t k = cdiv(count * splits, 256);
+      const double stages = double(cdiv(lines, splits));
+      double us = k == 1 ? stages * t.lone_stage + 3.0 : double(k) * (stages * t.stage + t.ends);
+      if (splits > 1) us += 3.0 + double(splits) * double(n) * double(m) * 8.0 / 4e6;
+      if (us < least) least = us, best = I8Plan{t.kind, 0, int(splits)};
+    }
+  }
+  return best;
+}
+
+// Whether the tokens are rounded within the product: it takes the place of a
+// launch and a pass through memory (1 token, 4096 -> 4096: 10.7 us, so 7.7; 4
+// tokens: 11.0, 9.4; 8 tokens of 1000: 6.6, 6.8), but every workgroup does it
+// (4 tokens, 2048 -> 28672: 20 us, so 40; 16 tokens of 1024: 7.1, 8.1).
+bool i8_fused(int64_t n, int64_t m, int64_t d) {
+  return n <= 8 && m <= 12288 && (16 / fused_waves(n)) * d <= 16384;
+}
+
+}  // namespace
+
+size_t matmul_i8_ws_bytes(int64_t m, int64_t d, int64_t n) {
+  const I8Plan p = i8_plan(n, m, d);
+  return p.splits > 1 ? size_t(p.splits) * n * m * sizeof(int32_t) : 0;
+}
 
 kq_status matmul_i8_run(const int8_t* a, const float* a_scale, const int32_t* a_sum, const int8_t* w,
                         const float* w_scale, const float* w_zero, const float* bias, int64_t n, int64_t m,
-                        int64_t d, void* y, kq_dtype dt, int64_t ldy, Arena&, hipStream_t s) {
+                        int64_t d, void* y, kq_dtype dt, int64_t ldy, Arena& ws, hipStream_t s) {
   const int64_t rb = i8_row_bytes(d);
   const I8Epi e{a_scale, a_sum, w_scale, w_zero, bias, n, m, ldy};
-  auto go = [&](auto* out) -> kq_status {
-    // Few tokens: the weights' bytes are what counts. 32 channels a workgroup
-    // where that still gives every CU one (12 tokens, 28672 -> 8192: 39.5 us
-    // against 47.6 us with 16), else 16 (1 token, 4096 -> 4096: 5.8 us
-    // against 6.5 us with 32).
-    if (n <= 32) {
-      const bool wide = m >= 32 * 256;
-      if (n <= 16) return wide ? stream_i8_launch<2, 1>(a, w, rb, e, out, s) : stream_i8_launch<1, 1>(a, w, rb, e, out, s);
-      return wide ? stream_i8_launch<2, 2>(a, w, rb, e, out, s) : stream_i8_launch<1, 2>(a, w, rb, e, out, s);
-    }
-    // The tile: the CU with most tiles takes ceil(tiles / 256) of them, one
-    // after the other, and a stage of a tile took 1.74 us (256 x 256), 0.99
-    // (128 x 256), 0.53 (128 x 128) and 0.23 us (64 x 64) at 8192 tokens,
-    // 28672 -> 8192; 2048 tokens, 4096 -> 11008, for one, take 117 us, 123,
-    // 123 and 183 with them, 512 tokens, 4096 -> 4096, 50, 32, 27 and 17 us.
-    auto cost = [&](int64_t tm, int64_t tn, double t) {
-      return double(cdiv(cdiv(n, tm) * cdiv(m, tn), 256)) * t;
+  const I8Plan p = i8_plan(n, m, d);
+  int32_t* partial = nullptr;
+  if (p.splits > 1) {
+    partial = ws.take<int32_t>(size_t(p.splits) * n * m);
+    if (!partial) return fail(KQ_ERR_WORKSPACE, "matmul_i8: workspace too small");
+  }
+  auto product = [&](auto* out) -> kq_status {
+    using Y = std::remove_pointer_t<decltype(out)>;
+    auto stream = [&](auto kernel, int waves) -> kq_status {
+      kernel<<<dim3(unsigned(cdiv(m, 16 * p.rt)), unsigned(p.splits)), 64 * waves, 0, s>>>(a, w, rb, e, out, partial);
+      KQ_HIP(hipGetLastError());
+      return KQ_OK;
     };
-    const double c1 = cost(256, 256, 1.74), c2 = cost(128, 256, 0.99), c3 = cost(128, 128, 0.53),
-                 c4 = cost(64, 64, 0.23);
-    if (c1 <= c2 && c1 <= c3 && c1 <= c4) return gemm_i8_launch<I8Tile<256, 256, 2, 4, 128, 2>>(a, w, rb, e, out, s);
-    if (c2 <= c3 && c2 <= c4) return gemm_i8_launch<I8Tile<128, 256, 2, 4, 128, 3>>(a, w, rb, e, out, s);
-    if (c3 <= c4) return gemm_i8_launch<I8Tile<128, 128, 2, 2, 128, 2>>(a, w, rb, e, out, s);
-    return gemm_i8_launch<I8Tile<64, 64, 2, 2, 128, 4>>(a, w, rb, e, out, s);
+    switch (p.kind) {
+      case I8_STREAM:
+        if (n <= 16) return stream(stream_i8_kernel<1, 1, 16, Y>, 16);
+        if (p.rt == 1) return stream(stream_i8_kernel<1, 2, 8, Y>, 8);
+        if (p.rt == 2) return stream(stream_i8_kernel<2, 2, 8, Y>, 8);
+        return stream(stream_i8_kernel<4, 2, 8, Y>, 8);
+      case I8_256: return gemm_i8_launch<I8Tile<256, 256, 2, 4, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);
+      case I8_128_256:
+        return gemm_i8_launch<I8Tile<128, 256, 2, 4, 128, 3>>(a, w, rb, e, out, p.splits, partial, s);
+      case I8_128: return gemm_i8_launch<I8Tile<128, 128, 2, 2, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);
+      default: return gemm_i8_launch<I8Tile<64, 64, 2, 2, 128, 4>>(a, w, rb, e, out, p.splits, partial, s);
+    }
+  };
+  auto go = [&](auto* out) -> kq_status {
+    KQ_TRY(product(out));
+    return p.splits > 1 ? join_i8_launch(partial, p.splits, e, out, s) : KQ_OK;
   };
   if (dt == KQ_BF16) return go(static_cast<uint16_t*>(y));
   return go(static_cast<float*>(y));
@@ -570,6 +835,7 @@ LinearWs linear_take(Arena& ar, int64_t n, int64_t d) {
 }  // namespace
 
 size_t linear_i8_ws_bytes(int64_t m, int64_t d, int64_t n) {
+  if (i8_fused(n, m, d)) return 0;
   Arena ar{nullptr, 0, 0};
   linear_take(ar, n, d);
   ar.take<char>(matmul_i8_ws_bytes(m, d, n));
@@ -579,6 +845,24 @@ size_t linear_i8_ws_bytes(int64_t m, int64_t d, int64_t n) {
 kq_status linear_i8_run(const void* x, kq_dtype dt, int64_t ldx, float clip, const int8_t* w,
                         const float* w_scale, const float* w_zero, const float* bias, int64_t n, int64_t m,
                         int64_t d, void* y, kq_dtype ydt, int64_t ldy, Arena& ws, hipStream_t s) {
+  if (i8_fused(n, m, d)) {
+    const int64_t rb = i8_row_bytes(d);
+    const I8Epi e{nullptr, nullptr, w_scale, w_zero, bias, n, m, ldy};
+    auto go = [&](auto* in, auto* out) -> kq_status {
+      using T = std::remove_const_t<std::remove_pointer_t<decltype(in)>>;
+      using Y = std::remove_pointer_t<decltype(out)>;
+      fused_i8_kernel<T, Y><<<unsigned(cdiv(m, 16)), 1024, size_t(n) * (rb + 16), s>>>(in, int(d), ldx, clip, w,
+                                                                                         rb, e, out);
+      KQ_HIP(hipGetLastError());
+      return KQ_OK;
+    };
+    auto with_y = [&](auto* in) -> kq_status {
+      if (ydt == KQ_BF16) return go(in, static_cast<uint16_t*>(y));
+      return go(in, static_cast<float*>(y));
+    };
+    if (dt == KQ_BF16) return with_y(static_cast<const uint16_t*>(x));
+    return with_y(static_cast<const float*>(x));
+  }
   const LinearWs l = linear_take(ws, n, d);
   if (!l.codes || !l.scale || !l.sums) return fail(KQ_ERR_WORKSPACE, "linear_i8: workspace too small");
   KQ_TRY(quantize_rows_run(x, dt, n, d, ldx, clip, l.codes, l.scale, l.sums, s));

@@ -107,9 +107,9 @@ CASES = [
     ("linear null x", lambda: lin(x=None), ARG, "NULL"),
     ("linear null y", lambda: lin(y=None), ARG, "NULL"),
     ("linear odd x", lambda: lin(x=ODD), ARG, "aligned to its type"),
-    ("linear no workspace", lambda: lin(ws=None), WS, "required"),
-    ("linear small workspace", lambda: lin(wsb=16), WS, "required"),
-    ("linear odd workspace", lambda: lin(ws=C + 8), ARG, "workspace must be 16-byte"),
+    ("linear no workspace", lambda: lin(n=40, ws=None), WS, "required"),
+    ("linear small workspace", lambda: lin(n=40, wsb=16), WS, "required"),
+    ("linear odd workspace", lambda: lin(n=40, ws=C + 8), ARG, "workspace must be 16-byte"),
     ("top dtype", lambda: top(dt=3), ARG, "dtype"),
     ("top rows", lambda: top(n=-1), SHAPE, "0 <= n"),
     ("top ld", lambda: top(ld=99), SHAPE, "vocab <= ld"),
@@ -174,7 +174,7 @@ def test_nothing_to_do_is_not_an_error():
     assert wsize(N.KQ_OP_LINEAR_I8, n=0) == N.KQ_OK
 
 
-@pytest.mark.parametrize("m,d,n", [(16, 64, 4), (300, 1001, 700), (8192, 28672, 12), (4096, 4096, 1)])
+@pytest.mark.parametrize("m,d,n", [(16, 64, 40), (300, 1001, 700), (8192, 28672, 12), (4096, 4096, 5), (256, 28672, 3), (8192, 28672, 64)])
 def test_workspace_one_byte_short(m, d, n):
     b = ctypes.c_size_t()
     for op, call in ((N.KQ_OP_LINEAR_I8, lin), (N.KQ_OP_MATMUL_I8, mm)):
