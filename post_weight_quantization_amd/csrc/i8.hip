@@ -47,6 +47,14 @@ struct __attribute__((packed, aligned(2))) Raw16 {
   uint32_t w[4];
 };
 
+// 16 bytes read once: past the caches' usual order (8192 tokens of 28672 bf16:
+// 125 us, else 140)
+typedef uint32_t Mem16 __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ Raw16 load_once(const void* p) {
+  const Mem16 v = __builtin_nontemporal_load(static_cast<const Mem16*>(p));
+  return {v.x, v.y, v.z, v.w};
+}
+
 // What a row's codes are made with. rint(v / s) asks for the correctly rounded
 // quotient; v * (1 / s) is off from it by at most 127 * 2^-22 = 3e-5, so where it
 // lies further than 1e-4 from a midpoint between two codes, both round to
@@ -123,7 +131,7 @@ __global__ __launch_bounds__(TPB) void quantize_rows_kernel(const T* __restrict_
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     q[i] = Raw16{};
-    if (i * TPB + t < full) q[i] = *reinterpret_cast<const Raw16*>(xr + int64_t(i * TPB + t) * E);
+    if (i * TPB + t < full) q[i] = load_once(xr + int64_t(i * TPB + t) * E);
   }
   float tail = 0.f;
   if (full * E + t < d) tail = load_f32(xr + full * E + t);
@@ -255,7 +263,7 @@ __device__ inline void i8_store(const v16i (&acc)[MI][NJ], const I8Epi& e, int64
   constexpr int W = 32 * MI;                              // channels of a wave
   constexpr int ROWB = W * 4 + 16;                        // padded: rows start in other banks
   constexpr int CH = 16 / int(sizeof(Y));                 // channels of a lane: 16 bytes of y
-  constexpr int LPR = W / CH;                             // lanes for a token's channels
+  constexpr int LPR = W / CH, RPP = 64 / LPR;             // lanes of a token's channels, tokens of a pass
   const int lane = threadIdx.x & 63, lt = lane & 31, lh = lane >> 5;
   const int64_t o = o0 + lane % LPR * CH;
   float ws[CH], bias[CH];
@@ -277,10 +285,10 @@ __device__ inline void i8_store(const v16i (&acc)[MI][NJ], const I8Epi& e, int64
             v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     wave_sync();  // the slab is the wave's own
 #pragma unroll 2
-    for (int p = 0; p < 32 * LPR / 64; ++p) {
-      const int row = p * (64 / LPR) + lane / LPR;
+    for (int p = 0; p < (32 + RPP - 1) / RPP; ++p) {
+      const int row = p * RPP + lane / LPR;
       const int64_t tk = t0 + 32 * j + row;
-      if (tk < e.n) {
+      if (lane < RPP * LPR && row < 32 && tk < e.n) {
         const v4i* src = reinterpret_cast<const v4i*>(slab + row * ROWB + lane % LPR * CH * 4);
         if (partial) {  // a share of K: the sums as they are
           int32_t* dst = partial + tk * e.m + o;
@@ -450,8 +458,8 @@ template <class C, class Y>
 kq_status gemm_i8_launch(const int8_t* a, const int8_t* w, int64_t rb, const I8Epi& e, Y* y, int splits,
                          int32_t* partial, hipStream_t s) {
   const auto kernel = gemm_i8_kernel<C, Y>;
-  KQ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                             C::LDS));
+  static std::atomic<uint64_t> allowed{0};
+  KQ_TRY(allow_lds(kernel, C::LDS, allowed));
   const dim3 grid(unsigned(8 * cdiv(cdiv(e.n, C::TM) * cdiv(e.m, C::TN), 8)), unsigned(splits));
   kernel<<<grid, 64 * C::NW, C::LDS, s>>>(a, w, rb, e, y, partial);
   KQ_HIP(hipGetLastError());
@@ -712,7 +720,7 @@ kq_status pack_i8_run(const uint8_t* codes, const float* zero, int64_t d_out, in
 namespace {
 
 // How a product is taken, by its sizes alone.
-enum I8Kind { I8_STREAM, I8_64, I8_128, I8_128_256, I8_256 };
+enum I8Kind { I8_STREAM, I8_64, I8_128, I8_128_256, I8_256_192, I8_256 };
 struct I8Plan {
   I8Kind kind;
   int rt;      // streams: 16-channel tiles of a workgroup
@@ -734,21 +742,23 @@ I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
     if (groups < 256 && lines >= 128) p.splits = int(std::min(cdiv(256, groups), lines / 64));
     return p;
   }
-  // The tile: the CU with most tiles takes k = ceil(tiles / 256) of them, each
-  // some time for every 128-byte stage of K and some at its ends. Fitted to
-  // 8192 tokens, 28672 -> 8192 (1562 us with 256 x 256, 1775, 1889 and 3241
-  // with 128 x 256, 128 x 128 and 64 x 64), 4096, 4096 -> 4096 (68, 83, 84,
-  // 126) and 512, 4096 -> 4096 (50, 32, 27, 17, where a CU has one of the small
-  // tiles for itself). With fewer tiles than CUs the stages are shared, for
-  // the launch that joins the sums and its traffic.
+  // The tile (tokens x channels): the CU with most tiles takes k = ceil(tiles /
+  // 256) of them, each some time for every 128-byte stage of K and some at
+  // its ends. Fitted to 8192 tokens, 28672 -> 8192 (1422 us with 256 x 256, 1785
+  // with 256 x 192, 1670, 1772 and 3241 with 128 x 256, 128 x 128 and 64 x 64),
+  // 2048 tokens, 4096 -> 11008 (115, 99, 106, 116 and 172) and 512, 4096 -> 4096
+  // (50 with 256 x 256, 32, 27 and 17, where a CU has one of the small tiles
+  // for itself). With fewer tiles than CUs the stages are shared, for the
+  // launch that joins the sums and its traffic.
   static const struct {
     I8Kind kind;
     int64_t tm, tn;
     double stage, ends, lone_stage;
-  } tiles[] = {{I8_256, 256, 256, 1.705, 5.0, 1.705},
-               {I8_128_256, 128, 256, 0.949, 9.5, 0.949},
-               {I8_128, 128, 128, 0.509, 4.0, 0.86},
-               {I8_64, 64, 64, 0.223, 0.7, 0.27}};
+  } tiles[] = {{I8_256, 256, 256, 1.55, 7.8, 1.55},
+               {I8_256_192, 256, 192, 1.29, 8.4, 1.29},
+               {I8_128_256, 128, 256, 0.90, 6.6, 0.95},
+               {I8_128, 128, 128, 0.476, 4.1, 0.86},
+               {I8_64, 64, 64, 0.21, 0.7, 0.27}};
   I8Plan best{I8_64, 0, 1};
   double least = 1e30;
   for (const auto& t : tiles) {
@@ -805,6 +815,8 @@ kq_status matmul_i8_run(const int8_t* a, const float* a_scale, const int32_t* a_
         if (p.rt == 2) return stream(stream_i8_kernel<2, 2, 8, Y>, 8);
         return stream(stream_i8_kernel<4, 2, 8, Y>, 8);
       case I8_256: return gemm_i8_launch<I8Tile<256, 256, 2, 4, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);
+      case I8_256_192:
+        return gemm_i8_launch<I8Tile<256, 192, 4, 2, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);
       case I8_128_256:
         return gemm_i8_launch<I8Tile<128, 256, 2, 4, 128, 3>>(a, w, rb, e, out, p.splits, partial, s);
       case I8_128: return gemm_i8_launch<I8Tile<128, 128, 2, 2, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);

@@ -2,6 +2,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstddef>
 
@@ -99,6 +100,18 @@ GemmArgs gemm_args(const float* A, int64_t lda, const float* B, int64_t ldb, flo
                    int64_t M, int64_t N, int64_t K, float alpha, float beta, uint32_t flags);
 
 // ------------------------------------------------------------ utilities
+// Lets `kernel` use `bytes` of dynamic LDS on the current device: asked for once
+// per device (`done`: a bit each, of the kernel's own) and kept by the runtime.
+template <class K>
+inline kq_status allow_lds(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  KQ_HIP(hipGetDevice(&dev));
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return KQ_OK;
+  KQ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return KQ_OK;
+}
 kq_status fill_f32(float* p, int64_t n, float v, hipStream_t s);
 // Copies `bytes` (at most 64) of device memory to the host once the stream's
 // earlier work is done: through a pinned per-thread buffer, polling the

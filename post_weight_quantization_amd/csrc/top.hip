@@ -283,15 +283,16 @@ kq_status top_logits_run(const void* logits, kq_dtype dt, int64_t n, int64_t voc
       return KQ_OK;
     };
     // Held in registers, in workgroups as small as take the row in 16 chunks
-    // a thread (4096 x 32000 bf16: 74 us with 256 threads, 90 with 512), and
-    // of the largest rows those that fit at all (4096 x 128256 bf16: 251 us,
-    // read twice 311). The number of rows has no say, so that a row's sum,
+    // a thread (4096 x 32000 bf16: 74 us with 256 threads, 90 with 512; 512 x
+    // 50001 fp32, lists of 200: 36.5 us with 16 chunks of 1024 threads, 38.2
+    // with 32 of 512), and the largest rows that fit too (4096 x 128256 bf16:
+    // 251 us, read twice 306). The number of rows has no say, so that a row's sum,
     // and its rounding, is the same in whatever company.
     if (chunks <= 1024) return go(Variant<4, 256, 6>());
     if (chunks <= 2048) return go(Variant<8, 256, 5>());
     if (chunks <= 4096) return go(Variant<16, 256, 4>());
     if (chunks <= 8192) return go(Variant<16, 512, 4>());
-    if (chunks <= 16384) return go(Variant<32, 512, 2>());
+    if (chunks <= 16384) return go(Variant<16, 1024, 4>());
     return go(Variant<0, 512, 6>());
   };
   if (dt == KQ_BF16) return launch(static_cast<const uint16_t*>(logits));
