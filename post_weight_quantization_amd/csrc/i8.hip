@@ -744,21 +744,24 @@ I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
   }
   // The tile (tokens x channels): the CU with most tiles takes k = ceil(tiles /
   // 256) of them, each some time for every 128-byte stage of K and some at
-  // its ends. Fitted to 8192 tokens, 28672 -> 8192 (1422 us with 256 x 256, 1785
-  // with 256 x 192, 1670, 1772 and 3241 with 128 x 256, 128 x 128 and 64 x 64),
-  // 2048 tokens, 4096 -> 11008 (115, 99, 106, 116 and 172) and 512, 4096 -> 4096
-  // (50 with 256 x 256, 32, 27 and 17, where a CU has one of the small tiles
-  // for itself). With fewer tiles than CUs the stages are shared, for the
-  // launch that joins the sums and its traffic.
+  // its ends; a CU's only tile has it for itself. Fitted to the times of every
+  // tile at 54 sizes, three of them: 8192 tokens, 28672 -> 8192 (1491 us with
+  // 256 x 256, 1840 with 256 x 192, 1703 and 1854 with 128 x 256 and 128 x 128),
+  // 2048 tokens, 4096 -> 11008 (120, 106, 111, 114, and 180 with 64 x 64) and
+  // 512, 4096 -> 4096 (52, 45, 33, 30 and 20). With fewer tiles than CUs the
+  // stages are shared, for the launch that joins the sums and its traffic (600
+  // tokens, 20000 -> 600: 30 us with 4 shares, 46 with one). The chosen tile is
+  // the fastest or within 5 % at 51 of the 54; the worst miss is 44 us for 34
+  // (136 tokens, 12463 -> 5530), where five CUs have two tiles, all others one.
   static const struct {
     I8Kind kind;
     int64_t tm, tn;
     double stage, ends, lone_stage;
-  } tiles[] = {{I8_256, 256, 256, 1.55, 7.8, 1.55},
-               {I8_256_192, 256, 192, 1.29, 8.4, 1.29},
-               {I8_128_256, 128, 256, 0.90, 6.6, 0.95},
-               {I8_128, 128, 128, 0.476, 4.1, 0.86},
-               {I8_64, 64, 64, 0.21, 0.7, 0.27}};
+  } tiles[] = {{I8_256, 256, 256, 1.55, 14.8, 1.58},
+               {I8_256_192, 256, 192, 1.16, 14.2, 1.28},
+               {I8_128_256, 128, 256, 0.86, 8.1, 0.87},
+               {I8_128, 128, 128, 0.485, 4.85, 0.80},
+               {I8_64, 64, 64, 0.256, 1.0, 0.285}};
   I8Plan best{I8_64, 0, 1};
   double least = 1e30;
   for (const auto& t : tiles) {
@@ -768,7 +771,7 @@ I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
       const int64_t k = cdiv(count * splits, 256);
       const double stages = double(cdiv(lines, splits));
       double us = k == 1 ? stages * t.lone_stage + 3.0 : double(k) * (stages * t.stage + t.ends);
-      if (splits > 1) us += 3.0 + double(splits) * double(n) * double(m) * 8.0 / 4e6;
+      if (splits > 1) us += 4.0 + double(splits) * double(n) * double(m) * 4e-6;
       if (us < least) least = us, best = I8Plan{t.kind, 0, int(splits)};
     }
   }

@@ -99,7 +99,12 @@ def test_quantize_rows_that_are_not_ordinary(dtype):
 SHAPES = [(1, 1, 1), (1, 64, 4096), (1, 4096, 128), (2, 100, 300), (7, 2777, 1001), (15, 512, 2048),
           (16, 130, 8192), (17, 96, 640), (33, 257, 129), (64, 1000, 4096), (100, 4097, 1024),
           (129, 255, 513), (300, 1024, 4096), (513, 1027, 777), (1500, 2050, 1100), (4100, 520, 256),
-          (40, 16, 65536), (4, 300, 28672), (24, 8192, 1024), (2048, 2816, 640)]
+          (40, 16, 65536), (4, 300, 28672), (24, 8192, 1024), (2048, 2816, 640),
+          # each tile, and each with K shared
+          (276, 27058, 68), (1030, 8200, 1000), (4129, 65, 16113), (2000, 10900, 500), (68, 4192, 11572),
+          (65, 2238, 15982), (40, 260, 30000), (600, 600, 20000),
+          # few tokens: 32 and 64 channels a workgroup, long rows shared
+          (30, 9000, 3000), (20, 16400, 400), (9, 1000, 20000), (4, 1000, 4096), (3, 12000, 4000)]
 
 
 @pytest.mark.parametrize("n,m,d", SHAPES)
