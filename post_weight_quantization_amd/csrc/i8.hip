@@ -467,37 +467,36 @@ kq_status gemm_i8_launch(const int8_t* a, const int8_t* w, int64_t rb, const I8E
 }
 
 // ------------------------------------------------------- few tokens
-// The codes of 16 RT channels stream from memory through the registers of SW
-// waves, which take the row's 128-byte lines in turn, and meet the codes of
-// 16 TT tokens (from L2) in v_mfma_i32_16x16x64_i8 (A: channels, B: tokens;
-// lane l holds 16 bytes of row l % 16 at k = 16 (l / 16), and of the result
-// channels 4 (l / 16) + r of token l % 16 in register r). The waves' sums
-// are joined in LDS: integers, in any order the same.
-template <int RT, int TT, int SW>
+// Up to 32 tokens: the channels' codes stream from memory through registers into
+// the matrix cores (no LDS, no barrier, every byte read once), 16 channels a
+// workgroup of SW waves, which share the 128-byte lines of a row and join their
+// sums in LDS: integers, in any order the same. In v_mfma_i32_16x16x64_i8 A is
+// the channels and B the tokens: lane l holds 16 bytes of row l % 16 at k = 16
+// (l / 16), and of the result channels 4 (l / 16) + r of token l % 16 in register
+// r. A wave's load is 16 rows of 64 bytes, four lines in flight (two with 32
+// tokens), neighbouring waves on neighbouring lines. 1 token, 28672 -> 8192: 43
+// us, 5.5 TB/s of codes: memory.
+template <int TT, int SW>
 struct StreamTile {
-  v4i acc[RT][TT];
+  v4i acc[TT];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < TT; ++t) acc[r][t] = v4i{0, 0, 0, 0};
+    for (int t = 0; t < TT; ++t) acc[t] = v4i{0, 0, 0, 0};
   }
-  // The sums of the workgroup's waves, joined: finish(sum, channel, token) for
-  // each, by one thread. part: SW * RT * TT * 64 vectors of LDS.
+  // A wave's sums for the others. part: SW * TT * 64 vectors of LDS.
+  __device__ __forceinline__ void leave(v4i* part, int wv, int lane) const {
+#pragma unroll
+    for (int t = 0; t < TT; ++t) part[(wv * TT + t) * 64 + lane] = acc[t];
+  }
+  // The sums of all waves, joined: finish(sum, channel, token) by one thread each.
   template <class F>
-  __device__ __forceinline__ void join(v4i* part, int wv, int lane, F finish) const {
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < TT; ++t) part[(wv * RT * TT + r * TT + t) * 64 + lane] = acc[r][t];
-    __syncthreads();
-    for (int j = threadIdx.x; j < RT * TT * 256; j += 64 * SW) {
-      const int c = j % (16 * RT), tk = j / (16 * RT);
-      const int tile = (c / 16) * TT + tk / 16, ln = (c % 16 / 4) * 16 + tk % 16;
+  __device__ static __forceinline__ void join(const v4i* part, F finish) {
+    for (int j = threadIdx.x; j < TT * 256; j += 64 * SW) {
+      const int c = j % 16, tk = j / 16, ln = (c / 4) * 16 + tk % 16;
       int sum = 0;
 #pragma unroll
-      for (int k = 0; k < SW; ++k) sum += part[(k * RT * TT + tile) * 64 + ln][c % 4];
+      for (int k = 0; k < SW; ++k) sum += part[(k * TT + tk / 16) * 64 + ln][c % 4];
       finish(sum, c, tk);
     }
   }
@@ -505,32 +504,30 @@ struct StreamTile {
 
 // gridDim.y workgroups share the lines of a row of codes; with more than one,
 // their sums go to `partial` (gridDim.y x n x m) and are joined afterwards.
-template <int RT, int TT, int SW, class Y>
+template <int TT, int SW, class Y>
 __global__ __launch_bounds__(64 * SW) void stream_i8_kernel(const int8_t* __restrict__ a,
                                                             const int8_t* __restrict__ w, int64_t rb, I8Epi e,
                                                             Y* __restrict__ y, int32_t* __restrict__ partial) {
-  __shared__ v4i part[SW * RT * TT * 64];
+  __shared__ v4i part[SW * TT * 64];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int64_t o0 = int64_t(blockIdx.x) * (16 * RT);
-  const int8_t *wp[RT], *ap[TT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) wp[r] = w + min(o0 + 16 * r + i, e.m - 1) * rb + 16 * g;
+  const int64_t o0 = int64_t(blockIdx.x) * 16;
+  const int8_t* wp = w + min(o0 + i, e.m - 1) * rb + 16 * g;
+  const int8_t* ap[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) ap[t] = a + min(int64_t(16 * t + i), e.n - 1) * rb + 16 * g;
-  StreamTile<RT, TT, SW> tile;
+  StreamTile<TT, SW> tile;
   tile.clear();
   constexpr int U = TT == 1 ? 4 : 2;  // 128-byte lines in flight
   const int lines = int(rb / 128), step = SW * int(gridDim.y);
   auto run = [&](int line, auto count) {
     constexpr int N = decltype(count)::value;
-    v4i fw[N][2][RT], fa[N][2][TT];
+    v4i fw[N][2], fa[N][2][TT];
 #pragma unroll
     for (int u = 0; u < N; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t k = int64_t(line + u * step) * 128 + 64 * h;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) fw[u][h][r] = *reinterpret_cast<const v4i*>(wp[r] + k);
+        fw[u][h] = *reinterpret_cast<const v4i*>(wp + k);
 #pragma unroll
         for (int t = 0; t < TT; ++t) fa[u][h][t] = *reinterpret_cast<const v4i*>(ap[t] + k);
       }
@@ -539,21 +536,91 @@ __global__ __launch_bounds__(64 * SW) void stream_i8_kernel(const int8_t* __rest
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int t = 0; t < TT; ++t)
-            tile.acc[r][t] =
-                __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][h][r], fa[u][h][t], tile.acc[r][t], 0, 0, 0);
+        for (int t = 0; t < TT; ++t)
+          tile.acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][h], fa[u][h][t], tile.acc[t], 0, 0, 0);
   };
   int line = int(blockIdx.y) * SW + wv;
   for (; line + (U - 1) * step < lines; line += U * step) run(line, std::integral_constant<int, U>());
   for (; line < lines; line += step) run(line, std::integral_constant<int, 1>());
-  tile.join(part, wv, lane, [&](int sum, int c, int tk) {
+  tile.leave(part, wv, lane);
+  __syncthreads();
+  tile.join(part, [&](int sum, int c, int tk) {
     const int64_t o = o0 + c;
     if (tk >= e.n || o >= e.m) return;
     if (gridDim.y > 1) partial[(int64_t(blockIdx.y) * e.n + tk) * e.m + o] = sum;
     else e.put(sum, tk, o, y);
   });
+}
+
+// The same where many channels meet several tokens. There every 16 channels
+// read all tokens' codes once more, and from the caches that takes as long as
+// the channels' own bytes do from memory (28672 -> 8192: 43 us with 1 token, 58
+// with 12, and 44 with 12 whose loads all take one line). So a workgroup keeps
+// its share of the tokens in registers, U lines a wave, U * SW at most, and
+// goes from 16 channels to the next, which are loaded while these are
+// multiplied: 12 tokens 48 us, with the launch that joins the shares; without
+// one (16 tokens, 4096 -> 32000) 27 us where each workgroup reads them 37.
+template <int TT, int U, int SW, class Y>
+__global__ __launch_bounds__(64 * SW) void kept_i8_kernel(const int8_t* __restrict__ a, const int8_t* __restrict__ w,
+                                                          int64_t rb, I8Epi e, Y* __restrict__ y,
+                                                          int32_t* __restrict__ partial) {
+  __shared__ v4i part[2][SW * TT * 64];  // by turns: a barrier for each 16 channels
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lines = int(rb / 128), tiles = int(cdiv(e.m, 16));
+  const int first = int(int64_t(lines) * blockIdx.y / gridDim.y);
+  const int end = int(int64_t(lines) * (blockIdx.y + 1) / gridDim.y);
+  // lines past the share: its last line of channels, zeros for tokens
+  int at[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) at[u] = min(first + wv + u * SW, end - 1) * 128;
+  auto load = [&](int t, v4i (&f)[U][2]) {
+    const int8_t* p = w + min(int64_t(min(t, tiles - 1)) * 16 + i, e.m - 1) * rb + 16 * g;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) f[u][h] = *reinterpret_cast<const v4i*>(p + at[u] + 64 * h);
+  };
+  v4i fa[U][2][TT], f0[U][2], f1[U][2];
+  int t = blockIdx.x;
+  load(t, f0);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < TT; ++q) {
+        const int8_t* p = a + min(int64_t(16 * q + i), e.n - 1) * rb + 16 * g + at[u] + 64 * h;
+        const v4i v = *reinterpret_cast<const v4i*>(p);
+        fa[u][h][q] = first + wv + u * SW < end ? v : v4i{0, 0, 0, 0};
+      }
+  auto step = [&](v4i (&f)[U][2], v4i (&ahead)[U][2], v4i* mine) {
+    load(t + int(gridDim.x), ahead);
+    StreamTile<TT, SW> tile;
+    tile.clear();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < TT; ++q)
+          tile.acc[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f[u][h], fa[u][h][q], tile.acc[q], 0, 0, 0);
+    tile.leave(mine, wv, lane);
+    // LDS alone: the loads stay in flight
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    tile.join(mine, [&](int sum, int c, int tk) {
+      const int64_t o = int64_t(t) * 16 + c;
+      if (tk >= e.n || o >= e.m) return;
+      if (gridDim.y > 1) partial[(int64_t(blockIdx.y) * e.n + tk) * e.m + o] = sum;
+      else e.put(sum, tk, o, y);
+    });
+    t += int(gridDim.x);
+    return t < tiles;
+  };
+  while (step(f0, f1, part[0]) && step(f1, f0, part[1])) {
+  }
 }
 
 // The smallest calls: the same with the tokens rounded on the way, by every
@@ -640,11 +707,11 @@ __global__ __launch_bounds__(1024) void fused_i8_kernel(const T* __restrict__ x,
   if (have && at == 0) scale[tok] = s;
   // ---- the product
   const int8_t* ap = codes + min(i, int(e.n) - 1) * rs + 16 * g;
-  StreamTile<1, 1, SW> tile;
+  StreamTile<1, SW> tile;
   tile.clear();
   auto mma = [&](const v4i& fw, int line, int h) {
     const v4i fa = *reinterpret_cast<const v4i*>(ap + line * 128 + 64 * h);
-    tile.acc[0][0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw, fa, tile.acc[0][0], 0, 0, 0);
+    tile.acc[0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw, fa, tile.acc[0], 0, 0, 0);
   };
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -660,7 +727,9 @@ __global__ __launch_bounds__(1024) void fused_i8_kernel(const T* __restrict__ x,
   }
   e.a_scale = scale;
   e.a_sum = sums;
-  tile.join(part, wv, lane, [&](int acc, int c, int tk) {
+  tile.leave(part, wv, lane);
+  __syncthreads();
+  tile.join(part, [&](int acc, int c, int tk) {
     if (tk < e.n && o0 + c < e.m) e.put(acc, tk, o0 + c, y);
   });
 }
@@ -720,27 +789,30 @@ kq_status pack_i8_run(const uint8_t* codes, const float* zero, int64_t d_out, in
 namespace {
 
 // How a product is taken, by its sizes alone.
-enum I8Kind { I8_STREAM, I8_64, I8_128, I8_128_256, I8_256_192, I8_256 };
+enum I8Kind { I8_STREAM, I8_KEPT, I8_64, I8_128, I8_128_256, I8_256_192, I8_256 };
 struct I8Plan {
   I8Kind kind;
-  int rt;      // streams: 16-channel tiles of a workgroup
   int splits;  // shares of K
 };
 
 I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
   const int64_t lines = cdiv(d, I8_PAD);
   if (n <= 32) {
-    // Few tokens: the weights' bytes are what counts. Up to 16 tokens take 16
-    // channels a workgroup (1 token, 8192 -> 28672: 41 us, with 32 channels
-    // 72; 12 tokens, 28672 -> 8192: 58, with 32 channels 56); with more, the
-    // tokens' own bytes are read less often the more channels meet them, as
-    // long as every CU has a workgroup (32 tokens, 8192 -> 28672: 89 us with 16
-    // channels, 73 with 32, 59 with 64; 4096 -> 4096: 9, 11 and 17). Long rows
-    // of few channels are shared (16 tokens, 28672 -> 1024: 30 us, shared 16).
-    I8Plan p{I8_STREAM, n <= 16 || m < 8192 ? 1 : m < 16384 ? 2 : 4, 1};
-    const int64_t groups = cdiv(m, 16 * p.rt);
-    if (groups < 256 && lines >= 128) p.splits = int(std::min(cdiv(256, groups), lines / 64));
-    return p;
+    // Few tokens: the channels' bytes are what counts, 16 channels a workgroup,
+    // until the tokens' bytes, read for each, cost more than keeping them in
+    // registers. That costs a second launch where the rows are longer than the
+    // 32 lines that a workgroup keeps: it is worth it from about 300000 lines
+    // of tokens on (4096 -> 14336, 112 lines: 10 tokens 17.6 us streamed and
+    // kept, 16 tokens 19.4 and 18.3; 8192 -> 28672: 6 tokens 48 and 47, 16
+    // tokens 64 and 48), else from 640 groups of channels on (1 token, 4096 ->
+    // 11008: 13.8 and 12.0; 2048 -> 8192: 4.1 and 4.7).
+    const int64_t groups = cdiv(m, 16), shares = cdiv(lines, 32);
+    if (shares == 1 ? groups >= 640 : groups >= 256 && groups * lines * n >= 300000)
+      return I8Plan{I8_KEPT, int(shares)};
+    // Long rows of few channels are shared (16 tokens, 8192 -> 1024: 10.2 us,
+    // shared by 4 7.6; 4096 -> 1024: 6.1, shared by 2 6.6).
+    if (groups < 256 && lines >= 64) return I8Plan{I8_STREAM, int(std::min(256 / groups, lines / 16))};
+    return I8Plan{I8_STREAM, 1};
   }
   // The tile (tokens x channels): the CU with most tiles takes k = ceil(tiles /
   // 256) of them, each some time for every 128-byte stage of K and some at
@@ -762,7 +834,7 @@ I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
                {I8_128_256, 128, 256, 0.86, 8.1, 0.87},
                {I8_128, 128, 128, 0.485, 4.85, 0.80},
                {I8_64, 64, 64, 0.256, 1.0, 0.285}};
-  I8Plan best{I8_64, 0, 1};
+  I8Plan best{I8_64, 1};
   double least = 1e30;
   for (const auto& t : tiles) {
     const int64_t count = cdiv(n, t.tm) * cdiv(m, t.tn);
@@ -772,7 +844,7 @@ I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
       const double stages = double(cdiv(lines, splits));
       double us = k == 1 ? stages * t.lone_stage + 3.0 : double(k) * (stages * t.stage + t.ends);
       if (splits > 1) us += 4.0 + double(splits) * double(n) * double(m) * 4e-6;
-      if (us < least) least = us, best = I8Plan{t.kind, 0, int(splits)};
+      if (us < least) least = us, best = I8Plan{t.kind, int(splits)};
     }
   }
   return best;
@@ -806,17 +878,31 @@ kq_status matmul_i8_run(const int8_t* a, const float* a_scale, const int32_t* a_
   }
   auto product = [&](auto* out) -> kq_status {
     using Y = std::remove_pointer_t<decltype(out)>;
-    auto stream = [&](auto kernel, int waves) -> kq_status {
-      kernel<<<dim3(unsigned(cdiv(m, 16 * p.rt)), unsigned(p.splits)), 64 * waves, 0, s>>>(a, w, rb, e, out, partial);
+    auto rows = [&](auto kernel, int waves, int64_t groups) -> kq_status {
+      kernel<<<dim3(unsigned(groups), unsigned(p.splits)), 64 * waves, 0, s>>>(a, w, rb, e, out, partial);
       KQ_HIP(hipGetLastError());
       return KQ_OK;
     };
+    const int64_t groups = cdiv(m, 16);
     switch (p.kind) {
       case I8_STREAM:
-        if (n <= 16) return stream(stream_i8_kernel<1, 1, 16, Y>, 16);
-        if (p.rt == 1) return stream(stream_i8_kernel<1, 2, 8, Y>, 8);
-        if (p.rt == 2) return stream(stream_i8_kernel<2, 2, 8, Y>, 8);
-        return stream(stream_i8_kernel<4, 2, 8, Y>, 8);
+        if (n <= 16) return rows(stream_i8_kernel<1, 16, Y>, 16, groups);
+        return rows(stream_i8_kernel<2, 8, Y>, 8, groups);
+      case I8_KEPT: {
+        // 16 waves a CU over all shares, each with 1 or 2 lines
+        const int64_t share = cdiv(rb / I8_PAD, p.splits);
+        const int64_t all = std::min<int64_t>(groups, 256 / p.splits);
+        if (share <= 8) {
+          if (n <= 16) return rows(kept_i8_kernel<1, 1, 8, Y>, 8, std::min<int64_t>(groups, 512));
+          return rows(kept_i8_kernel<2, 1, 8, Y>, 8, std::min<int64_t>(groups, 512));
+        }
+        if (share <= 16) {
+          if (n <= 16) return rows(kept_i8_kernel<1, 1, 16, Y>, 16, all);
+          return rows(kept_i8_kernel<2, 1, 16, Y>, 16, all);
+        }
+        if (n <= 16) return rows(kept_i8_kernel<1, 2, 16, Y>, 16, all);
+        return rows(kept_i8_kernel<2, 2, 16, Y>, 16, all);
+      }
       case I8_256: return gemm_i8_launch<I8Tile<256, 256, 2, 4, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);
       case I8_256_192:
         return gemm_i8_launch<I8Tile<256, 192, 4, 2, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);
