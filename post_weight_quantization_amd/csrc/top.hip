@@ -22,6 +22,8 @@
 // enough if everything else is at or above tau, as in a row whose mask
 // leaves few columns. What that does not settle (and a row with a NaN or +inf) is
 // searched bit by bit for the K-th largest key, counting.
+#include <type_traits>
+
 #include "logits_rows.h"
 
 namespace kq {
@@ -58,7 +60,7 @@ struct TopLds {
   uint32_t rank[LIST];
   Raw chunk[NW][CHUNKS];
   int chunk_no[NW][CHUNKS];
-  uint16_t group[GROUPS];
+  __align__(16) uint16_t group[GROUPS];
   int pivots[2][16];
   float part[NW];
   int ipart[2][NW];
@@ -145,40 +147,68 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
     g[0] = max3(g[0], r.tail, r.tail);
     float mine = g[0];
     for (int i = 1; i < GP; ++i) mine = max3(mine, g[i], g[i]);
-    if (k <= TPB / 4)
+    // a group for each thread will do for lists of up to a quarter as many
+    const bool few = k <= TPB / 4;
+    if (few)
       s.group[t] = uint16_t(key_of(mine) >> 16);
     else
       for (int i = 0; i < GP; ++i) s.group[i * TPB + t] = uint16_t(key_of(g[i]) >> 16);
+    // m, and a bound below tau: the lowest of the largest of K sets of threads
+    // or more, the sets as large as that leaves them
+    float m = mine, least = mine;
+    auto wider = [&](auto step) {
+      m = wave_step<decltype(step)::value>(m, Max());
+      if (TPB >> (decltype(step)::value + 1) >= k) least = m;
+    };
+    wider(std::integral_constant<int, 0>());
+    wider(std::integral_constant<int, 1>());
+    wider(std::integral_constant<int, 2>());
+    wider(std::integral_constant<int, 3>());
+    wider(std::integral_constant<int, 4>());
+    wider(std::integral_constant<int, 5>());
+    m = max3(m, LOWEST, LOWEST);
+    uint32_t low = wave_reduce(key_of(least) >> 16, Min());
+    if (lane == 0) s.part[w] = m, s.ipart[0][w] = int(low);
     if (t == 0) s.count = 0, s.overflow = 0;
-    float m = max3(mine, LOWEST, LOWEST);
-    m = block_reduce<TPB>(m, s.part, Max());
-    // ---- the K-th largest of them, from the top in steps of 4 bits
-    uint32_t key = 0;
+    __syncthreads();
+    for (int i = 0; i < NW; ++i) m = max3(m, s.part[i], s.part[i]), low = min(low, uint32_t(s.ipart[0][i]));
+    // ---- the K-th largest of them, from the top in steps of 4 bits, between
+    // the lowest and the highest (which seldom lie more than 8 bits apart)
+    uint32_t key = __builtin_amdgcn_readfirstlane(low);
+    const uint32_t high = __builtin_amdgcn_readfirstlane(key_of(m) >> 16);
+    const int bits = high > key ? 32 - __clz(int(high - key)) : 0;
     auto kth = [&](auto per_lane) {
       constexpr int G = decltype(per_lane)::value;
       uint32_t v[G];
-      for (int i = 0; i < G; ++i) v[i] = s.group[i * 64 + lane];
+      const uint32_t* pairs = reinterpret_cast<const uint32_t*>(s.group) + lane * (G / 2);
+      for (int i = 0; i < G; i += 2) v[i] = pairs[i / 2] & 0xffffu, v[i + 1] = pairs[i / 2] >> 16;
 #pragma unroll 1
-      for (int step = 0; step < 4; ++step) {
+      for (int step = (bits + 3) / 4 - 1; step >= 0; --step) {
 #pragma unroll 1
         for (int p = w; p < 16; p += NW) {
-          const uint32_t pivot = key + (uint32_t(p) << (12 - 4 * step));
+          const uint32_t pivot = key + (uint32_t(p) << (4 * step));
           int cnt = 0;
           for (int i = 0; i < G; ++i) cnt += __popcll(__ballot(v[i] >= pivot));
           if (lane == 0) s.pivots[step & 1][p] = cnt;
         }
         __syncthreads();
-        int best = 0;
-        for (int p = 1; p < 16; ++p) best = s.pivots[step & 1][p] >= k ? p : best;
-        key += uint32_t(best) << (12 - 4 * step);
+        // the highest pivot with K groups at or above it; all are above the first
+        const uint64_t enough = __ballot(s.pivots[step & 1][lane & 15] >= k) | 1;
+        key += uint32_t(31 - __clz(int(uint32_t(enough) & 0xffffu))) << (4 * step);
       }
     };
-    // a group for each thread will do for lists of up to a quarter as many
-    if (k <= TPB / 4) kth(std::integral_constant<int, TPB / 64>());
+    if (few) kth(std::integral_constant<int, TPB / 64>());
     else kth(std::integral_constant<int, GROUPS / 64>());
     // too few groups reach above -inf: so does tau
     const float tau = key <= (KEY_NEG_INF >> 16) ? -__builtin_inff() : value_of(key << 16);
-    // ---- candidates, and the sum of exponentials
+    // ---- candidates, and the sum of exponentials: 2^(x c - ref), ref the whole
+    // number next to m c, so that it is one operation and its rounding that of
+    // x c. Where m c is past 2^30, neighbouring numbers differ by 2^7 and more,
+    // and what is not equal to m counts for nothing: the same for any larger c,
+    // and one that keeps m c below 2^31 has no overflow.
+    float scale = c;
+    if (!(fabsf(m * c) < 0x1p30f)) scale = ldexpf(1.f, 30 - (int(__float_as_uint(m) >> 23 & 255) - 127));
+    const float ref = rintf(m * scale);
     float sum = 0.f;
     int held = 0;  // of this wave's chunks, in LDS
     r.template each<true>(lr, full, [&](int i, int ch, const float(&x)[E<T>], Raw q) {
@@ -190,7 +220,7 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
         held += __popcll(hits);
       }
       float part = 0.f;
-      for (int e = 0; e < E<T>; ++e) part += __builtin_amdgcn_exp2f((x[e] - m) * c);
+      for (int e = 0; e < E<T>; ++e) part += __builtin_amdgcn_exp2f(fmaf(x[e], scale, -ref));
       sum += part;
       // computed here, not where the sum is used: the elements would be kept
       asm volatile("" : "+v"(sum));
@@ -206,7 +236,7 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
       if (take && at < LIST) s.list[at] = entry_of(v, j);
     };
     append(r.tail >= tau && full * E<T> + t < vocab, r.tail, full * E<T> + t);
-    sum += __builtin_amdgcn_exp2f((r.tail - m) * c);
+    sum += __builtin_amdgcn_exp2f(fmaf(r.tail, scale, -ref));
     if (more) r.load_tail(nr, full, vocab);
     if (held > CHUNKS) s.overflow = 1;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -221,7 +251,10 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
     }
     sum = block_reduce<TPB>(sum, s.part, Sum());
     // (no finite logit: the sum is 0)
-    if (lse && t == 0) lse[row] = sum == 0.f ? -__builtin_inff() : m * inv_t + logf(sum);
+    if (lse && t == 0) {
+      const float shift = fmaf(-m, scale, ref) * 0.69314718055994530942f;
+      lse[row] = sum == 0.f ? -__builtin_inff() : m * inv_t + (logf(sum) + shift);
+    }
     int count = s.count;
     if (s.overflow || count > LIST || sum != sum) {
       __syncthreads();
