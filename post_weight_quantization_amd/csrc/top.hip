@@ -118,7 +118,7 @@ __device__ void search(const T* row, int vocab, int k, TopLds<TPB / 64>& s) {
 }
 
 template <class T, class V>
-__global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* __restrict__ logits, int64_t n, int vocab,
+__global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* __restrict__ logits, int n, int vocab,
                                                          int64_t ld, int k, float inv_t,
                                                          float* __restrict__ values,
                                                          int32_t* __restrict__ index,
@@ -132,9 +132,9 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
   const float c = inv_t * 1.44269504088896340736f;
   Row<T, V> r;
   r.load(logits + int64_t(blockIdx.x) * ld, full, vocab);
-  for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
-    const T* lr = logits + row * ld;
-    const bool more = row + gridDim.x < n;
+  for (int row = blockIdx.x; row < n; row += gridDim.x) {
+    const T* lr = logits + int64_t(row) * ld;
+    const bool more = row + int(gridDim.x) < n;
     const int ahead = more ? full : 0;
     const T* nr = lr + (more ? int64_t(gridDim.x) * ld : 0);
     // ---- the largest of each group
@@ -219,8 +219,8 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
         if (hit && at < CHUNKS) s.chunk[w][at] = q, s.chunk_no[w][at] = ch;
         held += __popcll(hits);
       }
-      float part = 0.f;
-      for (int e = 0; e < E<T>; ++e) part += __builtin_amdgcn_exp2f(fmaf(x[e], scale, -ref));
+      float part = __builtin_amdgcn_exp2f(fmaf(x[0], scale, -ref));
+      for (int e = 1; e < E<T>; ++e) part += __builtin_amdgcn_exp2f(fmaf(x[e], scale, -ref));
       sum += part;
       // computed here, not where the sum is used: the elements would be kept
       asm volatile("" : "+v"(sum));
@@ -291,8 +291,8 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
     for (int i = t; i < count; i += TPB) {
       const uint32_t at = s.rank[i];
       if (at < uint32_t(k)) {
-        values[row * k + at] = value_of(uint32_t(s.list[i] >> 32));
-        index[row * k + at] = int32_t(~uint32_t(s.list[i]));
+        values[int64_t(row) * k + at] = value_of(uint32_t(s.list[i] >> 32));
+        index[int64_t(row) * k + at] = int32_t(~uint32_t(s.list[i]));
       }
     }
     __syncthreads();
@@ -310,7 +310,7 @@ kq_status top_logits_run(const void* logits, kq_dtype dt, int64_t n, int64_t voc
     const int64_t chunks = cdiv(vocab, E<T>);
     auto go = [&](auto v) -> kq_status {
       using V = decltype(v);
-      top_logits_kernel<T, V><<<row_groups<V>(n), V::TPB, 0, s>>>(p, n, int(vocab), ld, k, 1.f / temperature,
+      top_logits_kernel<T, V><<<row_groups<V>(n), V::TPB, 0, s>>>(p, int(n), int(vocab), ld, k, 1.f / temperature,
                                                                   values, index, lse);
       KQ_HIP(hipGetLastError());
       return KQ_OK;
