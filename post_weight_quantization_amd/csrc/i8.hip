@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "kq_internal.h"
+#include "lanes.h"
 
 namespace kq {
 
@@ -139,8 +140,7 @@ __global__ __launch_bounds__(TPB) void quantize_rows_kernel(const T* __restrict_
 #pragma unroll
   for (int i = 0; i < CH; ++i) m = Chunk::largest(m, q[i]);
   m = Chunk::own(m);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(m, o)));
+  m = wave_reduce(m, Max());
   if (lane == 0) pm[w] = m;
   __syncthreads();
 #pragma unroll
@@ -164,8 +164,7 @@ __global__ __launch_bounds__(TPB) void quantize_rows_kernel(const T* __restrict_
     sum += code;
     cr[k] = int8_t(code);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  sum = wave_reduce(sum, Sum());
   if (lane == 0) ps[w] = sum;
   __syncthreads();
   if (t == 0) {
@@ -647,12 +646,6 @@ __global__ __launch_bounds__(1024) void fused_i8_kernel(const T* __restrict__ x,
   const int64_t o0 = int64_t(blockIdx.x) * 16;
   const int lines = int(rb / 128), rs = int(rb) + 16;
   const int8_t* wp = w + min(o0 + i, e.m - 1) * rb + 16 * g;
-  v4i first[U][2];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      first[u][h] = *reinterpret_cast<const v4i*>(wp + int64_t(min(wv + u * SW, lines - 1)) * 128 + 64 * h);
   // ---- the tokens: wave wv takes part of token wv / wpt
   const int wpt = fused_waves(e.n), tok = wv / wpt, at = (wv % wpt) * 64 + lane, step = 64 * wpt;
   const bool have = tok < e.n;
@@ -666,15 +659,20 @@ __global__ __launch_bounds__(1024) void fused_i8_kernel(const T* __restrict__ x,
   }
   float tail = 0.f;
   if (have && full * E + at < d) tail = load_f32(xr + full * E + at);
+  v4i first[U][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      first[u][h] = *reinterpret_cast<const v4i*>(wp + int64_t(min(wv + u * SW, lines - 1)) * 128 + 64 * h);
   uint32_t m = __float_as_uint(fabsf(tail));
 #pragma unroll
   for (int k = 0; k < CH; ++k) m = Chunk::largest(m, q[k]);
   m = Chunk::own(m);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(m, o)));
+  m = wave_reduce(m, Max());
   if (lane == 0) pm[wv] = m;
   __syncthreads();
-  for (int k = 0; k < wpt; ++k) m = max(m, pm[tok * wpt + k]);
+  m = wave_reduce(pm[tok * wpt + (lane & (wpt - 1))], Max());
   const float s = i8_scale(m, clip);
   const I8Grid grid(s);
   int8_t* cr = codes + tok * rs;
@@ -695,16 +693,13 @@ __global__ __launch_bounds__(1024) void fused_i8_kernel(const T* __restrict__ x,
       cr[k] = int8_t(code);
     }
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  sum = wave_reduce(sum, Sum());
   if (lane == 0) ps[wv] = sum;
   __syncthreads();
-  if (threadIdx.x < e.n) {
-    int total = 0;
-    for (int k = 0; k < wpt; ++k) total += ps[threadIdx.x * wpt + k];
-    sums[threadIdx.x] = total;
+  if (have && wv % wpt == 0) {
+    sum = wave_reduce(lane < wpt ? ps[tok * wpt + lane] : 0, Sum());
+    if (lane == 0) scale[tok] = s, sums[tok] = sum;
   }
-  if (have && at == 0) scale[tok] = s;
   // ---- the product
   const int8_t* ap = codes + min(i, int(e.n) - 1) * rs + 16 * g;
   StreamTile<1, SW> tile;
