@@ -48,8 +48,8 @@ def _check_top(logits, k, temperature=1.0):
     wv, wi, wl = head.top_logits(_np(logits), k, temperature)
     np.testing.assert_array_equal(host(i), wi)
     np.testing.assert_array_equal(host(v), wv.astype(np.float32))
-    with np.errstate(invalid="ignore"):
-        ok = (np.abs(host(lse) - wl) <= 4e-5 + 2.0 ** -22 * np.abs(wl)) | (host(lse) == wl) | \
+    with np.errstate(invalid="ignore", over="ignore"):  # a sum past fp32 is inf
+        ok = (np.abs(host(lse) - wl) <= 4e-5 + 2.0 ** -22 * np.abs(wl)) | (host(lse) == wl.astype(np.float32)) | \
              (np.isnan(host(lse)) & np.isnan(wl))
     assert ok.all(), (host(lse), wl)
 
@@ -91,6 +91,23 @@ def test_top_logits_masked_and_not_finite(dtype):
     t[5, 7] = INF
     t[6, 0::2] = -INF
     _check_top(t, 20)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", [1e-4, 1.0, 300.0])
+def test_top_logits_of_any_magnitude(temperature, dtype):
+    """Rows far from zero, up to the type's largest numbers of either sign, and
+    temperatures that take logits / T past them. The bound of the other tests:
+    m / T in three roundings, 2^-22 of it; the logarithm of the sum, terms of
+    which count down to 2^-25, within 25 * 2^-23 and the sum's own roundings."""
+    top = torch.finfo(getattr(torch, DT[dtype])).max
+    offsets = [0.0, 30.0, -2000.0, 1e5, -7e8, 8e8, 1e20, 0.5 * top, -0.5 * top]
+    rng = np.random.default_rng(3)
+    t = torch.tensor(np.array([o + rng.normal(0, 3, 2500) * max(1.0, abs(o) / 256) for o in offsets]),
+                     dtype=torch.float64, device="cuda").to(getattr(torch, DT[dtype]))
+    t[1, 100:] = -top
+    t[7, 50:] = -INF
+    _check_top(t, 16, temperature)
 
 
 def _case(n, v, k, dtype, seed, stride=0, rest=False, temperature=1.0, ragged=False):
