@@ -19,6 +19,7 @@
 namespace kq {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(4)));  // at any word
 typedef int v16i __attribute__((ext_vector_type(16)));
 
 namespace {
@@ -28,11 +29,7 @@ constexpr int I8_PAD = 128;  // code rows are padded to this many bytes
 __device__ inline float bf16_f32(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
 
 // nearest even; a NaN stays a NaN
-__device__ inline uint16_t f32_bf16(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return uint16_t((u >> 16) | 0x40);
-  return uint16_t((u + 0x7fff + ((u >> 16) & 1)) >> 16);
-}
+__device__ inline uint16_t f32_bf16(float f) { return __builtin_bit_cast(uint16_t, __bf16(f)); }
 
 template <class T>
 __device__ inline float load_f32(const T* p);
@@ -265,6 +262,16 @@ __device__ inline void i8_store(const v16i (&acc)[MI][NJ], const I8Epi& e, int64
   constexpr int LPR = W / CH, RPP = 64 / LPR;             // lanes of a token's channels, tokens of a pass
   const int lane = threadIdx.x & 63, lt = lane & 31, lh = lane >> 5;
   const int64_t o = o0 + lane % LPR * CH;
+  // the tokens' scales and sums, a lane each
+  constexpr int TR = (32 * NJ + 63) / 64;
+  float as[TR];
+  int32_t sums[TR];
+#pragma unroll
+  for (int r = 0; r < TR; ++r) {
+    const int64_t tk = min(t0 + 64 * r + lane, e.n - 1);
+    as[r] = partial ? 0.f : e.a_scale[tk];
+    sums[r] = e.w_zero && !partial ? e.a_sum[tk] : 0;
+  }
   float ws[CH], bias[CH];
   int32_t wz[CH];
 #pragma unroll
@@ -283,32 +290,36 @@ __device__ inline void i8_store(const v16i (&acc)[MI][NJ], const I8Epi& e, int64
         *reinterpret_cast<v4i*>(slab + lt * ROWB + (32 * i + 8 * q + 4 * lh) * 4) =
             v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     wave_sync();  // the slab is the wave's own
-#pragma unroll 2
+#pragma unroll 4
     for (int p = 0; p < (32 + RPP - 1) / RPP; ++p) {
       const int row = p * RPP + lane / LPR;
       const int64_t tk = t0 + 32 * j + row;
+      const float a = __shfl(as[j / 2], 32 * (j % 2) + (row & 31));
+      const int32_t sum = __shfl(sums[j / 2], 32 * (j % 2) + (row & 31));
       if (lane < RPP * LPR && row < 32 && tk < e.n) {
         const v4i* src = reinterpret_cast<const v4i*>(slab + row * ROWB + lane % LPR * CH * 4);
         if (partial) {  // a share of K: the sums as they are
           int32_t* dst = partial + tk * e.m + o;
 #pragma unroll
-          for (int k = 0; k < CH; ++k)
-            if (o + k < e.m) dst[k] = src[k / 4][k % 4];
+          for (int q = 0; q < CH / 4; ++q) {
+            if (o + 4 * q + 4 <= e.m) *reinterpret_cast<v4i_any*>(dst + 4 * q) = src[q];
+            else
+              for (int k = 0; k < 4; ++k)
+                if (o + 4 * q + k < e.m) dst[4 * q + k] = src[q][k];
+          }
           continue;
         }
-        const float as = e.a_scale[tk];
-        const int32_t sum = e.w_zero ? e.a_sum[tk] : 0;
         Y v[CH];
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-          const float f = float(src[k / 4][k % 4] - wz[k] * sum) * as * ws[k];
-          store_y(v + k, e.bias ? f + bias[k] : f);
+          // (both factors have 24 bits)
+          store_y(v + k, float(src[k / 4][k % 4] - __mul24(wz[k], sum)) * a * ws[k] + bias[k]);
         }
         Y* dst = y + tk * e.ldy + o;
         if (o + CH <= e.m) {
-          Raw16 r;
+          Mem16 r;
           __builtin_memcpy(&r, v, 16);
-          *reinterpret_cast<Raw16*>(dst) = r;
+          __builtin_nontemporal_store(r, reinterpret_cast<Mem16*>(dst));
         } else {
           for (int k = 0; k < CH; ++k)
             if (o + k < e.m) dst[k] = v[k];
@@ -729,21 +740,32 @@ __global__ __launch_bounds__(1024) void fused_i8_kernel(const T* __restrict__ x,
   });
 }
 
-// y from the sums that `splits` workgroups left
+// y from the sums that `splits` workgroups left, 4 channels a thread
 template <class Y>
 __global__ __launch_bounds__(256) void join_i8_kernel(const int32_t* __restrict__ partial, int splits, I8Epi e,
                                                       Y* __restrict__ y) {
-  const int64_t per = cdiv(e.m, 256), t = blockIdx.x / per;
-  const int64_t o = (blockIdx.x - t * per) * 256 + threadIdx.x;
+  const int64_t per = cdiv(e.m, 1024), t = blockIdx.x / per;
+  const int64_t o = (blockIdx.x - t * per) * 1024 + 4 * threadIdx.x;
   if (o >= e.m) return;
-  int sum = 0;
-  for (int k = 0; k < splits; ++k) sum += partial[(int64_t(k) * e.n + t) * e.m + o];
-  e.put(sum, t, o, y);
+  const int32_t* p = partial + t * e.m + o;
+  const int64_t share = e.n * e.m;
+  if (o + 4 <= e.m) {
+    v4i sum = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) sum += *reinterpret_cast<const v4i_any*>(p + k * share);
+    for (int i = 0; i < 4; ++i) e.put(sum[i], t, o + i, y);
+  } else {
+    for (int i = 0; o + i < e.m; ++i) {
+      int sum = 0;
+      for (int k = 0; k < splits; ++k) sum += p[k * share + i];
+      e.put(sum, t, o + i, y);
+    }
+  }
 }
 
 template <class Y>
 kq_status join_i8_launch(const int32_t* partial, int splits, const I8Epi& e, Y* y, hipStream_t s) {
-  join_i8_kernel<<<unsigned(cdiv(e.m, 256) * e.n), 256, 0, s>>>(partial, splits, e, y);
+  join_i8_kernel<<<unsigned(cdiv(e.m, 1024) * e.n), 256, 0, s>>>(partial, splits, e, y);
   KQ_HIP(hipGetLastError());
   return KQ_OK;
 }
@@ -812,23 +834,23 @@ I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
   // The tile (tokens x channels): the CU with most tiles takes k = ceil(tiles /
   // 256) of them, each some time for every 128-byte stage of K and some at
   // its ends; a CU's only tile has it for itself. Fitted to the times of every
-  // tile at 54 sizes, three of them: 8192 tokens, 28672 -> 8192 (1491 us with
-  // 256 x 256, 1840 with 256 x 192, 1703 and 1854 with 128 x 256 and 128 x 128),
-  // 2048 tokens, 4096 -> 11008 (120, 106, 111, 114, and 180 with 64 x 64) and
-  // 512, 4096 -> 4096 (52, 45, 33, 30 and 20). With fewer tiles than CUs the
-  // stages are shared, for the launch that joins the sums and its traffic (600
-  // tokens, 20000 -> 600: 30 us with 4 shares, 46 with one). The chosen tile is
-  // the fastest or within 5 % at 51 of the 54; the worst miss is 44 us for 34
-  // (136 tokens, 12463 -> 5530), where five CUs have two tiles, all others one.
+  // tile at 54 sizes, three of them: 8192 tokens, 28672 -> 8192 (1442 us with
+  // 256 x 256, 1683 with 256 x 192, 1621 and 1802 with 128 x 256 and 128 x 128),
+  // 2048 tokens, 4096 -> 11008 (101, 88, 96, 95, and 150 with 64 x 64) and 512,
+  // 4096 -> 4096 (45, 38, 29, 27 and 18). With fewer tiles than CUs the stages
+  // are shared, for the launch that joins the sums and its traffic (600 tokens,
+  // 20000 -> 600: 27 us with 4 shares, 46 with one). The chosen tile is the
+  // fastest or within 3 % at 50 of the 54; the worst miss is 23 us for 21 (73
+  // tokens, 7856 -> 4159).
   static const struct {
     I8Kind kind;
     int64_t tm, tn;
     double stage, ends, lone_stage;
-  } tiles[] = {{I8_256, 256, 256, 1.55, 14.8, 1.58},
-               {I8_256_192, 256, 192, 1.16, 14.2, 1.28},
-               {I8_128_256, 128, 256, 0.86, 8.1, 0.87},
-               {I8_128, 128, 128, 0.485, 4.85, 0.80},
-               {I8_64, 64, 64, 0.256, 1.0, 0.285}};
+  } tiles[] = {{I8_256, 256, 256, 1.2, 10.8, 1.4},
+               {I8_256_192, 256, 192, 1.035, 8.0, 1.17},
+               {I8_128_256, 128, 256, 0.785, 5.3, 0.89},
+               {I8_128, 128, 128, 0.444, 3.25, 0.83},
+               {I8_64, 64, 64, 0.267, 0.98, 0.293}};
   I8Plan best{I8_64, 1};
   double least = 1e30;
   for (const auto& t : tiles) {
@@ -838,7 +860,7 @@ I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
       const int64_t k = cdiv(count * splits, 256);
       const double stages = double(cdiv(lines, splits));
       double us = k == 1 ? stages * t.lone_stage + 3.0 : double(k) * (stages * t.stage + t.ends);
-      if (splits > 1) us += 4.0 + double(splits) * double(n) * double(m) * 4e-6;
+      if (splits > 1) us += 3.0 + double(splits) * double(n) * double(m) * 2.6e-6;
       if (us < least) least = us, best = I8Plan{t.kind, int(splits)};
     }
   }

@@ -102,6 +102,7 @@ SHAPES = [(1, 1, 1), (1, 64, 4096), (1, 4096, 128), (2, 100, 300), (7, 2777, 100
           (40, 16, 65536), (4, 300, 28672), (24, 8192, 1024), (2048, 2816, 640),
           # each tile, and each with K shared
           (276, 27058, 68), (1030, 8200, 1000), (4129, 65, 16113), (2000, 10900, 500), (68, 4192, 11572),
+          (140, 23126, 64), (4155, 67, 8009),
           (65, 2238, 15982), (40, 260, 30000), (600, 600, 20000),
           # few tokens, kept in registers (1, 2 lines of each of 8, 16 waves; shared) and not (long rows shared)
           (7, 11000, 1000), (20, 16400, 400), (3, 10500, 1500), (31, 10300, 2000), (10, 10300, 3000),
