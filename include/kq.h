@@ -14,6 +14,9 @@
  *   kq_cholesky_inv     upper U with U^T U = (H_X' + delta I)^-1
  *   kq_gptaq_quantize   blocked column sweep onto a 2/3/4-bit grid
  *   kq_allocate_bits    widths by descending s under an average-bit budget
+ *   kq_linear_i8        a layer in 8-bit integers, one token or many
+ *   kq_top_logits, kq_distill_loss_grad   the divergence from a teacher's
+ *                       answers and its gradient (a G for H_G)
  *
  * Conventions (all calls):
  *  - Matrices are dense and row-major; the row stride equals the column
@@ -29,8 +32,10 @@
  *    per calling thread (hipHostMalloc on first use, kept until the process
  *    ends) through which the calls below read their host results, and the
  *    host copy of the last launch schedule kq_accumulate_cov built on the
- *    thread (rebuilt when the shapes or the requested outputs change);
- *    nothing else carries over from one call to the next.
+ *    thread (rebuilt when the shapes or the requested outputs change), and
+ *    a bit per device for each kernel of the 8-bit product whose LDS size
+ *    has been asked for; nothing else carries over from one call to the
+ *    next.
  *  - Device work is enqueued on `stream` and is asynchronous, except calls
  *    that return host values: kq_sensitivity and kq_layer_objective wait
  *    until the stream is idle before returning; kq_cholesky_inv waits for

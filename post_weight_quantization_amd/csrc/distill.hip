@@ -8,13 +8,17 @@
 //   dL/ds_j = w T [ c_j q_j - p_j ],   c_j = P on the list, P - r / q_r off it,
 //   P = sum p + r.
 //
-// A workgroup holds its row on chip (logits_rows.h), so the logits are read
-// once and the gradient written once: the largest logit m and the sum of
+// A workgroup takes a row (logits_rows.h): the largest logit m and the sum of
 // e_j = exp((s_j - m) / T) in one pass, and e_j again times one factor of the row,
 //   w T (P / sum e - r / sum of e off the list),
 // which is the gradient of every column off the list; the K columns on it
-// are written again after a barrier. The teacher's side is computed by the
-// first K threads while the row is on its way.
+// are written again after a barrier. For loss and gradient in one call rows of
+// up to 128 KB stay in registers between the passes, so the logits are read
+// once and the gradient written once: memory bounds it (4096 x 32000 bf16: 110
+// us, 4.8 TB/s; copying runs at 5.2). Longer rows are read twice (8192 x 128256
+// bf16: 916 us, 4.6 TB/s of one read and one write, the second read beside
+// them). The teacher's side is computed by the first K threads while the row
+// is on its way.
 //
 // What decides a small loss is kept from cancelling: m goes off before the
 // scaling, e is summed apart for the columns on and off the list (a bit per
@@ -249,9 +253,15 @@ kq_status distill_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab,
     const std::false_type no;
     // What is chosen goes by the row's length alone, so that a row's sums, and
     // their rounding, are the same in whatever company.
-    // One pass, nothing to hold: loss of 4096 x 32000 bf16 58 us with 256
-    // threads, 72 with 512; 4096 x 128256: 160, 164 (few rows: 16 x 32000 11, 9).
-    if (!grad) return chunks <= 4096 ? go(Variant<0, 256, 6>(), yes, no) : go(Variant<0, 512, 6>(), yes, no);
+    // One pass, nothing to hold: loss of 20000 x 4000 bf16 66 us with 256 threads
+    // and room for 8 waves, 74 with 6; of 4096 x 32000 54 with 256 and 6, 59 with
+    // 8, 66 with 512 threads; of 1 x 128256 24 with 256, 16 with 512, and of 4096
+    // of them 162 and 172.
+    if (!grad) {
+      if (chunks <= 1024) return go(Variant<0, 256, 8>(), yes, no);
+      if (chunks <= 4096) return go(Variant<0, 256, 6>(), yes, no);
+      return go(Variant<0, 512, 6>(), yes, no);
+    }
     if (!loss) {
       // gradient of 8192 x 4000 bf16: 52 us with 256 threads, 75 with 512; 4096
       // x 32000: 107, 103; 4096 x 128256: 417, 405, 392 with 1024
@@ -260,10 +270,10 @@ kq_status distill_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab,
       return go(Variant<0, 1024, 8>(), no, yes);
     }
     // Loss and gradient: two passes. Rows of up to 128 KB are held in
-    // registers (4096 x 32000 bf16: 115 us, read twice 126; 4096 x 65536: 220,
-    // 234); of longer ones a CU holds too few at once to keep the memory
+    // registers (4096 x 32000 bf16: 117 us, read twice 128; 4096 x 65536: 224,
+    // 232); of longer ones a CU holds too few at once to keep the memory
     // busy, and the second pass finds them in the cache beside it (4096 x
-    // 128256: 463 us, in registers 531 to 599).
+    // 128256: 453 us, in registers 531 to 599).
     if (chunks <= 512) return go(Variant<2, 256, 6>(), yes, yes);
     if (chunks <= 1024) return go(Variant<4, 256, 6>(), yes, yes);
     if (chunks <= 2048) return go(Variant<8, 256, 5>(), yes, yes);

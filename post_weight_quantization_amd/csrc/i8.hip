@@ -202,15 +202,22 @@ struct I8Epi {
 };
 
 // ---------------------------------------------------------------- the GEMM
-// A workgroup of 4 waves owns TM tokens x TN channels, each wave a quarter of
-// them in tiles of v_mfma_i32_32x32x32_i8 (A: channels, B: tokens; lane l
-// holds 16 bytes of row l % 32 at k = 16 (l / 32), and of the result channels
-// 8 (r / 4) + 4 (l / 32) + r % 4 of token l % 32 in register r).
+// Many tokens: a workgroup owns TM tokens x TN channels, each of its WT x WO
+// waves a part of them in tiles of v_mfma_i32_32x32x32_i8 (A: channels, B:
+// tokens; lane l holds 16 bytes of row l % 32 at k = 16 (l / 32), and of the
+// result channels 8 (r / 4) + 4 (l / 32) + r % 4 of token l % 32 in register r).
 //
-// Stages of 64 bytes of K of all rows stream from memory straight into LDS
-// through a ring of NST slots. 16-byte chunk c of row r lies at
-// c ^ (r / 4 % 4) of its 64 bytes, so that the 16 lanes that LDS serves
-// together, 16 rows at one c, touch 16 different groups of banks.
+// Stages of 128 bytes of K of all rows stream from memory straight into LDS
+// through a ring of NST slots (64 bytes in a ring of 4: 10 % slower at 8192
+// tokens, 28672 -> 8192). 16-byte chunk c of row r lies at c ^ (r / 2 % 8) of
+// its 128 bytes, so that the 16 lanes that LDS serves together, 16 rows at one
+// c, touch different groups of banks.
+//
+// At 8192 tokens, 28672 -> 8192, tiles of 256 x 256 reach 2.7 POP/s: a stage
+// takes some 2600 cycles, its MFMAs 2048, at the 1.9 GHz that the part holds
+// under this load; 8 waves (4 waves of 128 x 128 need fewer LDS reads but have
+// nothing to run beside their own waits: 2.2 POP/s).
+
 // 16 bytes per lane from base + off into LDS: lane l's at lds_addr + 16 l.
 // Complete once vmcnt has counted the load down.
 __device__ inline void dma16(const int8_t* base, uint32_t off, uint32_t lds_addr) {
@@ -232,11 +239,11 @@ __device__ inline void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-template <int TM_, int TN_, int WT_, int WO_, int KB_, int NST_>
+template <int TM_, int TN_, int WT_, int WO_, int NST_>
 struct I8Tile {
   static constexpr int TM = TM_, TN = TN_;           // tokens, channels of a workgroup
   static constexpr int WT = WT_, WO = WO_;           // its waves along them
-  static constexpr int KB = KB_;                     // bytes of K of a stage
+  static constexpr int KB = 128;                     // bytes of K of a stage
   static constexpr int NST = NST_;                   // slots of the ring
   static constexpr int NW = WT * WO, MI = TN / WO / 32, NJ = TM / WT / 32;
   static constexpr int STB = (TM + TN) * KB;
@@ -245,14 +252,17 @@ struct I8Tile {
   static constexpr int SLAB = 32 * (32 * MI * 4 + 16);  // bytes a wave turns its results round in
   static constexpr int LDS = NST * STB > NW * SLAB ? NST * STB : NW * SLAB;
   // the chunk swizzle of a row
-  static __device__ int swz(int row) { return KB == 64 ? row >> 2 & 3 : row >> 1 & 7; }
+  static __device__ int swz(int row) { return row >> 1 & 7; }
 };
 
 // y from the sums of a wave's tiles: 32 tokens at a time go through LDS as
 // they are, so that a lane then has the same few channels of token after
 // token, with their scales in registers, and a wave writes whole runs of a
 // token's channels. The fp32 conversion of the sum, the two scales and the
-// bias each round once; y is rounded to its type after that.
+// bias each round once; y is rounded to its type after that. Nothing is loaded
+// within the passes (with the tokens' scales read there, and the sums rounded
+// in software, a tile of 256 x 192 took 29000 cycles, now 19000), and y goes past
+// the caches' usual order (14000: what 256 CUs write at once takes memory 11000).
 template <int MI, int NJ, class Y>
 __device__ inline void i8_store(const v16i (&acc)[MI][NJ], const I8Epi& e, int64_t t0, int64_t o0,
                                 char* slab, Y* y, int32_t* partial) {
@@ -920,13 +930,13 @@ kq_status matmul_i8_run(const int8_t* a, const float* a_scale, const int32_t* a_
         if (n <= 16) return rows(kept_i8_kernel<1, 2, 16, Y>, 16, all);
         return rows(kept_i8_kernel<2, 2, 16, Y>, 16, all);
       }
-      case I8_256: return gemm_i8_launch<I8Tile<256, 256, 2, 4, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);
+      case I8_256: return gemm_i8_launch<I8Tile<256, 256, 2, 4, 2>>(a, w, rb, e, out, p.splits, partial, s);
       case I8_256_192:
-        return gemm_i8_launch<I8Tile<256, 192, 4, 2, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);
+        return gemm_i8_launch<I8Tile<256, 192, 4, 2, 2>>(a, w, rb, e, out, p.splits, partial, s);
       case I8_128_256:
-        return gemm_i8_launch<I8Tile<128, 256, 2, 4, 128, 3>>(a, w, rb, e, out, p.splits, partial, s);
-      case I8_128: return gemm_i8_launch<I8Tile<128, 128, 2, 2, 128, 2>>(a, w, rb, e, out, p.splits, partial, s);
-      default: return gemm_i8_launch<I8Tile<64, 64, 2, 2, 128, 4>>(a, w, rb, e, out, p.splits, partial, s);
+        return gemm_i8_launch<I8Tile<128, 256, 2, 4, 3>>(a, w, rb, e, out, p.splits, partial, s);
+      case I8_128: return gemm_i8_launch<I8Tile<128, 128, 2, 2, 2>>(a, w, rb, e, out, p.splits, partial, s);
+      default: return gemm_i8_launch<I8Tile<64, 64, 2, 2, 4>>(a, w, rb, e, out, p.splits, partial, s);
     }
   };
   auto go = [&](auto* out) -> kq_status {

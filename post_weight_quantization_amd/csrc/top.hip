@@ -11,17 +11,23 @@
 //      waves counting for 16 pivots side by side.
 //   2. Chunks with an element at or above tau go to LDS, each wave's to a
 //      part of its own (places by ballot, no atomics to wait for), while the
-//      exponentials are summed and the next row is loaded in their place (64
-//      of 4096 x 128256 bf16: 268 us; with the sums in the first pass, after
-//      which the loads begin later, 329 us); their elements at or above tau then make
-//      a list. An element is the 64-bit key (order of its value, complement
-//      of its index), so no two are equal, and its rank is the number of
-//      larger keys on the list.
+//      exponentials are summed and the next row is loaded in their place (with
+//      the sums in the first pass, after which the loads begin later, 64 of 4096
+//      x 128256 bf16 took 329 us where this order took 268); their elements at
+//      or above tau then make a list. An element is the 64-bit key (order of its
+//      value, complement of its index), so no two are equal, and its rank is the
+//      number of larger keys on the list.
 // Should either overflow (128 chunks of a wave, 1024 elements: many equal
-// logits), a second pass takes what is above tau and, of the first K columns, what equals it:
-// enough if everything else is at or above tau, as in a row whose mask
-// leaves few columns. What that does not settle (and a row with a NaN or +inf) is
-// searched bit by bit for the K-th largest key, counting.
+// logits), a second pass takes what is above tau and, of the first K columns,
+// what equals it: enough where that makes K of them, as in a row whose mask
+// leaves few columns. What that does not settle (and a row with a NaN or +inf)
+// is searched bit by bit for the K-th largest key, counting.
+//
+// 64 of 4096 x 128256 bf16 take 206 us, 5.1 TB/s; vector instructions bound it:
+// they keep the SIMDs busy 83 % of the time, half of that an exponential per
+// element, at a quarter of the rate of the others. One row alone takes its CU 13
+// us, spent the same way; it is not shared among CUs, whose sums would join in an
+// order that many rows do not have.
 #include <type_traits>
 
 #include "logits_rows.h"
@@ -316,10 +322,10 @@ kq_status top_logits_run(const void* logits, kq_dtype dt, int64_t n, int64_t voc
       return KQ_OK;
     };
     // Held in registers, in workgroups as small as take the row in 16 chunks
-    // a thread (4096 x 32000 bf16: 74 us with 256 threads, 90 with 512; 512 x
-    // 50001 fp32, lists of 200: 36.5 us with 16 chunks of 1024 threads, 38.2
+    // a thread (4096 x 32000 bf16: 64 us with 256 threads, 98 with 512; 512 x
+    // 50001 fp32, lists of 200: 31.7 us with 16 chunks of 1024 threads, 34.1
     // with 32 of 512), and the largest rows that fit too (4096 x 128256 bf16:
-    // 251 us, read twice 306). The number of rows has no say, so that a row's sum,
+    // 208 us, read twice 290). The number of rows has no say, so that a row's sum,
     // and its rounding, is the same in whatever company.
     if (chunks <= 1024) return go(Variant<4, 256, 6>());
     if (chunks <= 2048) return go(Variant<8, 256, 5>());
