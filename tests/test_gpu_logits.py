@@ -262,6 +262,34 @@ def test_gradient_against_differences_of_the_gpu_losses():
         assert err < 4 * h * h + 2e-5 / h, err
 
 
+def test_rest_of_a_list_of_nearly_all_the_mass():
+    """A sure teacher at a temperature, t / T near 80 where fp32 steps are
+    7.6e-6: t / T of the list rounds as in the log-sum-exp that the caller
+    took, so the rest (5e-5 to 1e-3) is what these two leave. Bound of the
+    listed column's gradient T (q P - p), of terms near 1: an exponential (2^-23)
+    and four roundings on either side of the difference, 1e-6."""
+    n, v, T = 64, 1000, 0.7
+    rng = np.random.default_rng(8)
+    others = rng.normal(0, 3, (n, v)) + rng.uniform(30, 40, (n, 1))
+    rest = np.geomspace(5e-5, 1e-3, n)
+    others[:, 5] = -1e9
+    sure = T * (np.log(np.exp(others / T - 50).sum(1)) + 50 - np.log(rest))
+    others[:, 5] = sure
+    teacher = torch.tensor(others, dtype=torch.float32, device="cuda")
+    student = teacher + torch.tensor(rng.normal(0, 0.3, (n, v)), dtype=torch.float32, device="cuda")
+    scaled = teacher * (torch.ones((), device="cuda") / T)
+    lse = torch.logsumexp(scaled, 1)
+    idx = torch.full((n, 1), 5, dtype=torch.int32, device="cuda")
+    val = teacher[:, 5:6].contiguous()
+    _, grad = kq.kq_distill_loss_grad(student, val, idx, t_lse=lse, temperature=T)
+    T64 = float(np.float32(T))
+    as_rounded = host(scaled[:, 5:6]).astype(np.float64) * T64
+    _, want, _ = head.distill(host(student), as_rounded, host(idx), host(lse), T64, None)
+    assert np.abs(want[:, 5]).max() > 1e-5
+    err = np.abs(host(grad)[:, 5] - want[:, 5]).max()
+    assert err <= 1e-6, err
+
+
 def test_no_rows_and_graph_replays():
     e = torch.empty(0, 50, device="cuda")
     v, i, lse = kq.kq_top_logits(e, 4)
