@@ -69,6 +69,7 @@ struct TopLds {
   __align__(16) uint16_t group[GROUPS];
   int pivots[2][16];
   float part[NW];
+  float sums[NW];  // apart from `part`, which a wave may still read when another is done with the row
   int ipart[2][NW];
   int count, overflow;
 };
@@ -255,7 +256,7 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
       const float v = __uint_as_float(E<T> == 4 ? word : e & 1 ? word & 0xffff0000u : word << 16);
       append(i < items && v >= tau, v, s.chunk_no[w][at] * E<T> + e);
     }
-    sum = block_reduce<TPB>(sum, s.part, Sum());
+    sum = block_reduce<TPB>(sum, s.sums, Sum());
     // (no finite logit: the sum is 0)
     if (lse && t == 0) {
       const float shift = fmaf(-m, scale, ref) * 0.69314718055994530942f;
