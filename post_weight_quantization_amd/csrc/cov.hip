@@ -86,9 +86,11 @@ __device__ inline int swz(int r) { return 4 * (r & 3); }
 // LDS DMA: lane l's 16 bytes at gptr land at LDS byte address lds_addr + 16 l
 // (lds_addr is wave-uniform).
 // Issued through asm so the compiler does not wait for it before unrelated LDS
-// reads; completion is awaited explicitly with s_waitcnt vmcnt.
+// reads; completion is awaited explicitly with s_waitcnt vmcnt. (A write of m0
+// needs a wait state before the load that takes it; the compiler puts none
+// within asm.)
 __device__ inline void dma16(const void* gptr, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
                : "v"(gptr), "s"(__builtin_amdgcn_readfirstlane(lds_addr))
                : "memory", "m0");

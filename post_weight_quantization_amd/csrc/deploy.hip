@@ -727,9 +727,11 @@ typedef int v8i_t __attribute__((ext_vector_type(8)));
 typedef float v4f_t __attribute__((ext_vector_type(4)));
 
 // 16 bytes per lane from global memory straight into LDS: lane i's land at
-// lds_addr + 16 i. Complete once vmcnt has counted the load down.
+// lds_addr + 16 i. Complete once vmcnt has counted the load down. (A write of m0
+// needs a wait state before the load that takes it; the compiler puts none
+// within asm.)
 __device__ inline void a4_dma16(const void* gptr, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
                : "v"(gptr), "s"(__builtin_amdgcn_readfirstlane(lds_addr))
                : "memory", "m0");

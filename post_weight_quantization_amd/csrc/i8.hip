@@ -219,9 +219,10 @@ struct I8Epi {
 // nothing to run beside their own waits: 2.2 POP/s).
 
 // 16 bytes per lane from base + off into LDS: lane l's at lds_addr + 16 l.
-// Complete once vmcnt has counted the load down.
+// Complete once vmcnt has counted the load down. (A write of m0 needs a wait
+// state before the load that takes it; the compiler puts none within asm.)
 __device__ inline void dma16(const int8_t* base, uint32_t off, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
                : "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds_addr))
                : "memory", "m0");
