@@ -461,6 +461,7 @@ kq_status kq_linear_i8(const void* x, kq_dtype dt, int64_t ldx, float clip, cons
  * index; a NaN counts as larger than any number, +0 and -0 as equal):
  *   values  n x k floats;  index  n x k int32
  *   lse     n floats: log sum_j exp(logits_j / T) over the whole row, or NULL
+ *           (+inf where a logit is +inf and none is NaN)
  * k <= vocab <= 2^30. */
 kq_status kq_top_logits(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld,
                         int32_t k, float temperature, float* values, int32_t* index, float* lse,

@@ -56,6 +56,9 @@ def top_logits(logits, k, temperature=1.0):
         index[i] = order[:k]
         values[i] = z[i, order[:k]]
         m = np.max(z[i])
+        if m == np.inf:  # (a NaN in the row makes m NaN)
+            lse[i] = np.inf
+            continue
         m = 0.0 if m == -np.inf else m
         with np.errstate(divide="ignore"):
             lse[i] = m / temperature + np.log(np.sum(np.exp((z[i] - m) / temperature)))

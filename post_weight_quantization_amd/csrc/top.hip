@@ -257,8 +257,9 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
       append(i < items && v >= tau, v, s.chunk_no[w][at] * E<T> + e);
     }
     sum = block_reduce<TPB>(sum, s.sums, Sum());
-    // (no finite logit: the sum is 0)
-    if (lse && t == 0) {
+    // (no finite logit: the sum is 0; NaN: the row's largest, found below, is the
+    // answer)
+    if (lse && t == 0 && sum == sum) {
       const float shift = fmaf(-m, scale, ref) * 0.69314718055994530942f;
       lse[row] = sum == 0.f ? -__builtin_inff() : m * inv_t + (logf(sum) + shift);
     }
@@ -298,7 +299,9 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
     for (int i = t; i < count; i += TPB) {
       const uint32_t at = s.rank[i];
       if (at < uint32_t(k)) {
-        values[int64_t(row) * k + at] = value_of(uint32_t(s.list[i] >> 32));
+        const float v = value_of(uint32_t(s.list[i] >> 32));
+        values[int64_t(row) * k + at] = v;
+        if (at == 0 && lse && sum != sum) lse[row] = v;  // +inf, or NaN, which is above it
         index[int64_t(row) * k + at] = int32_t(~uint32_t(s.list[i]));
       }
     }

@@ -47,3 +47,28 @@ def test_top_logits_of_rows_whose_groups_agree(n, v, dtype):
     lower = -(-v // 3)
     want = c.double() + np.log(v - lower + lower * np.exp(-1.0))
     assert ((lse.double() - want).abs() <= 4e-5 + 2.0 ** -22 * want.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("v", [11, 900, 40000, 140000])
+def test_log_sum_exp_of_rows_with_infinities(v, dtype):
+    """+inf where a logit is +inf, NaN where one is NaN, -inf where none is
+    above it; the lists as ever."""
+    rng = np.random.default_rng(v)
+    z = rng.normal(0, 2, (7, v))
+    z[0, v - 1] = INF
+    z[1, 3], z[1, v // 2] = INF, INF
+    z[2, 2], z[2, v - 2] = INF, np.nan
+    z[3, 1] = np.nan
+    z[4, :] = -INF
+    z[5, :v - 2], z[5, v - 2] = -INF, INF
+    t = torch.tensor(z, dtype=torch.float32, device="cuda").to(getattr(torch, DT[dtype]))
+    for temperature in (1.0, 0.3):
+        values, index, lse = kq.kq_top_logits(t, 9, temperature)
+        wv, wi, wl = head.top_logits(_np(t), 9, temperature)
+        np.testing.assert_array_equal(host(index), wi)
+        np.testing.assert_array_equal(host(values), wv.astype(np.float32))
+        got = host(lse)
+        assert got[0] == INF and got[1] == INF and got[5] == INF and got[4] == -INF
+        assert np.isnan(got[2]) and np.isnan(got[3])
+        assert abs(got[6] - wl[6]) <= 4e-5 + 2.0 ** -22 * abs(wl[6])
