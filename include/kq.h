@@ -490,7 +490,9 @@ kq_status kq_distill_loss(const void* logits, kq_dtype dt, int64_t n, int64_t vo
                           float* stats, hipStream_t stream);
 
 /* The gradient from the stats of the forward call and the gradient of each
- * row's loss (dloss, n floats, in place of w above).
+ * row's loss (dloss, n floats, in place of w above). log q_r being fp32, the r
+ * term of a column may be off by up to 2^-21 |log q_r| of itself; it is left out
+ * where log q_r is -inf (or at the end of fp32's range).
  *   grad    n x vocab of the logits' type with row stride ldg >= vocab; it
  *           may be the logits themselves (ldg = ld). */
 kq_status kq_distill_grad(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld,

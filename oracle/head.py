@@ -103,8 +103,16 @@ def distill(logits, values, index, t_lse=None, temperature=1.0, weight=None):
                 r = 1.0 - total
             on = np.zeros(v, bool)
             on[[j for j, _ in entries]] = True
-            q_off = np.sum(q[~on])
-            stats[i] = m, log_sum, np.log(q_off)
+            # against the largest off the list: its mass may lie far below
+            # what a number can hold beside 1
+            m_off = np.max(s[i][~on], initial=-np.inf)
+            if m_off == -np.inf:
+                log_q_off, share = -np.inf, np.zeros(v)
+            else:
+                e_off = np.where(on, 0.0, np.exp((np.where(on, m_off, s[i]) - m_off) / T))
+                log_q_off = (m_off - m) / T + np.log(np.sum(e_off)) - log_sum
+                share = e_off / np.sum(e_off)  # q_j / q_r
+            stats[i] = m, log_sum, log_q_off
             value = 0.0
             for (j, _), lp in zip(entries, log_p):
                 p = np.exp(lp)
@@ -112,10 +120,9 @@ def distill(logits, values, index, t_lse=None, temperature=1.0, weight=None):
                     value += p * (lp - log_q[j])
                 grad[i, j] -= p
             if r > 0:
-                value += r * (np.log(r) - np.log(q_off))
+                value += r * (np.log(r) - log_q_off)
             P = total + r
-            c_off = P - r / q_off if r > 0 and q_off > 0 else P
-            grad[i] += q * np.where(on, P, c_off)
+            grad[i] += q * P - r * share
             loss[i] = w * T * T * value
             grad[i] *= w * T
     return loss, grad, stats

@@ -8,11 +8,14 @@
 //   dL/ds_j = w T [ c_j q_j - p_j ],   c_j = P on the list, P - r / q_r off it,
 //   P = sum p + r.
 //
-// A workgroup takes a row (logits_rows.h): the largest logit m and the sum of
-// e_j = exp((s_j - m) / T) in one pass, and e_j again times one factor of the row,
-//   w T (P / sum e - r / sum of e off the list),
-// which is the gradient of every column off the list; the K columns on it
-// are written again after a barrier. For loss and gradient in one call rows of
+// A workgroup takes a row (logits_rows.h). One pass finds the largest logit m'
+// off the list and the sum of e_j = exp((s_j - m') / T) there; the K listed
+// logits make the sum on it, from a maximum of their own, and both join to
+// the sum of the row. e_j again times one factor of the row,
+//   w T (P q_r - r) / sum of e off the list,
+// is the gradient of every column off the list; the K columns on it
+// are written again after a barrier. (Without a bucket every column counts as
+// off the list, and the factor is w T P / sum e.) For loss and gradient in one call rows of
 // up to 128 KB stay in registers between the passes, so the logits are read
 // once and the gradient written once: memory bounds it (4096 x 32000 bf16: 110
 // us, 4.8 TB/s; copying runs at 5.2). Longer rows are read twice (8192 x 128256
@@ -20,11 +23,14 @@
 // them). The teacher's side is computed by the first K threads while the row
 // is on its way.
 //
-// What decides a small loss is kept from cancelling: m goes off before the
+// What decides a small loss is kept from cancelling: the maxima go off before the
 // scaling, e is summed apart for the columns on and off the list (a bit per
 // column in LDS says which), never as a difference of sums, and the remainder
 // 1 - sum p, the sum of the loss's terms and the factors of the gradient are
-// joined in 64 bits. Exponentials and logarithms are the hardware's in fp32.
+// joined in 64 bits. And from vanishing: off the list e is taken against the
+// largest there, so q_r may be as small as the distance of the two maxima makes it
+// (against the row's largest it was 0, and the loss +inf, from 87 T on).
+// Exponentials and logarithms are the hardware's in fp32.
 #include "logits_rows.h"
 
 namespace kq {
@@ -43,8 +49,23 @@ constexpr double LN2 = 0.69314718055994530942;
 __device__ inline float uniform(float v) {
   return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
 }
+__device__ inline double uniform(double v) {
+  return __hiloint2double(__builtin_amdgcn_readfirstlane(__double2hiint(v)),
+                          __builtin_amdgcn_readfirstlane(__double2loint(v)));
+}
 
 __device__ inline float masked(float v, uint32_t keep) { return __uint_as_float(__float_as_uint(v) & keep); }
+
+// one value of the columns off the list, one of those on it
+struct Pair {
+  float off, on;
+};
+struct PairMax {
+  __device__ Pair operator()(Pair a, Pair b) const { return {Max()(a.off, b.off), Max()(a.on, b.on)}; }
+};
+struct PairSum {
+  __device__ Pair operator()(Pair a, Pair b) const { return {a.off + b.off, a.on + b.on}; }
+};
 
 struct DistillArgs {
   int64_t n, ld, ldg;
@@ -63,7 +84,8 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
   constexpr int CH = V::CH, TPB = V::TPB;
   extern __shared__ uint32_t bits[];  // a bit per column: on the list
   __shared__ double dpart[2][TPB / 64];
-  __shared__ float fpart[5][TPB / 64];
+  __shared__ float fpart[2][TPB / 64];
+  __shared__ Pair pair[2][TPB / 64];
   __shared__ __align__(16) int idx_at[K_MAX];
   __shared__ __align__(16) float p_at[K_MAX];
   static_assert(K_MAX <= TPB, "one thread per entry of the list");
@@ -113,115 +135,152 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
       asm volatile("" : "+v"(scaled));
       log_p = (scaled - d.t_lse[row]) * LOG2E;
     } else {
-      float tm = block_reduce<TPB>(tv, fpart[3], Max());
+      float tm = block_reduce<TPB>(tv, fpart[0], Max());
       if (tm == -__builtin_inff()) tm = 0.f;
       const float z = (tv - tm) * c;
-      const float total = block_reduce<TPB>(__builtin_amdgcn_exp2f(z), fpart[4], Sum());
+      const float total = block_reduce<TPB>(__builtin_amdgcn_exp2f(z), fpart[1], Sum());
       log_p = z - __builtin_amdgcn_logf(total);
       if (total == 0.f) mass = 0.0;
     }
     const float p = idx >= 0 ? __builtin_amdgcn_exp2f(log_p) : 0.f;
     if (t < d.k) p_at[t] = p;
     if (bucket) {
-      mass = block_reduce<TPB>(double(p), dpart[0], Sum());
+      mass = uniform(block_reduce<TPB>(double(p), dpart[0], Sum()));
       rest = 1.0 - mass;
       if (rest <= REST_MIN) rest = 0.0;
       mass += rest;
     } else {
       __syncthreads();
     }
-    // entries of one column: the first writes for all
+    // entries of one column: the first counts and writes for all
     float p_col = 0.f;
-    bool writes = GRAD && idx >= 0;
-    if (writes) {
+    bool first = (GRAD || bucket) && idx >= 0;
+    if (first) {
       for (int l = 0; l < d.k; l += 4) {
         const int4 other = *reinterpret_cast<const int4*>(idx_at + l);
-        const float4 po = *reinterpret_cast<const float4*>(p_at + l);
-        p_col += (other.x == idx ? po.x : 0.f) + (other.y == idx ? po.y : 0.f) +
-                 (other.z == idx ? po.z : 0.f) + (other.w == idx ? po.w : 0.f);
+        if (GRAD) {
+          const float4 po = *reinterpret_cast<const float4*>(p_at + l);
+          p_col += (other.x == idx ? po.x : 0.f) + (other.y == idx ? po.y : 0.f) +
+                   (other.z == idx ? po.z : 0.f) + (other.w == idx ? po.w : 0.f);
+        }
         if ((other.x == idx && l < t) || (other.y == idx && l + 1 < t) || (other.z == idx && l + 2 < t) ||
             (other.w == idx && l + 3 < t))
-          writes = false;
+          first = false;
       }
     }
     // ---- the student's side
-    auto on_list = [&](int ch) {
+    // listed elements of a chunk become -inf (in registers for good: their
+    // gradient comes from the list)
+    auto without_listed = [&](int ch, Raw& q) {
+      if (!bucket || ch >= full) return;
       const int j = ch * E<T>;
-      return bits[j >> 5] >> (j & 31) & ((1u << E<T>) - 1);
+      const uint32_t mark = bits[j >> 5] >> (j & 31) & ((1u << E<T>) - 1);
+      if (mark)
+        for (int i = 0; i < 4; ++i) {
+          uint32_t listed = uint32_t(__builtin_amdgcn_sbfe(int(mark), E<T> / 4 * i, 1));
+          if (E<T> == 8) {  // two halves
+            const uint32_t upper = uint32_t(__builtin_amdgcn_sbfe(int(mark), 2 * i + 1, 1));
+            listed = __builtin_amdgcn_perm(upper, listed, 0x05040100u);
+          }
+          q[i] = (q[i] & ~listed) | (neg_inf_word<T>() & listed);
+        }
     };
-    float m, total, off;
+    // m: the row's largest logit, total: the sum of exp((s - m) / T), q_r: the mass
+    // off the list. There a column's share of q_r is exp2((s - ref) c - log_ref) / off.
+    float m, total, q_r, off, ref, log_ref;
     if (LOSS) {
       Online o;
-      float on = 0.f, top = max3(r.tail, LOWEST, LOWEST);
+      float top = LOWEST;
       off = 0.f;
-      auto rescale = [&](float f) { on *= f, off *= f; };
-      r.template each<!GRAD>(lr, full, [&](int, int ch, const float(&x)[E<T>], Raw) {
-        const float here = max_of(x);
-        top = max3(top, here, here);
-        o.raise(here, c, rescale);
-        float e[E<T>], part = 0.f;
-        for (int i = 0; i < E<T>; ++i) part += e[i] = __builtin_amdgcn_exp2f((x[i] - o.m) * c);
-        const uint32_t mark = bucket && ch < full ? on_list(ch) : 0;
-        if (mark) {
-          part = 0.f;
-          for (int i = 0; i < E<T>; ++i) {
-            if (mark >> i & 1) on += e[i];
-            else part += e[i];
-          }
-        }
-        off += part;
-      });
-      o.raise(r.tail, c, rescale);
+      auto rescale = [&](float f) { off *= f; };
+      r.template each<!GRAD>(
+          lr, full,
+          [&](int, int, const float(&x)[E<T>], Raw) {
+            const float here = max_of(x);
+            top = max3(top, here, here);
+            o.raise(here, c, rescale);
+            float part = 0.f;
+            for (int i = 0; i < E<T>; ++i) part += __builtin_amdgcn_exp2f((x[i] - o.m) * c);
+            off += part;
+            // computed here, not where the sum is used: the elements would be kept
+            asm volatile("" : "+v"(off));
+          },
+          without_listed);
       const int j = full * E<T> + t;
-      const float e = __builtin_amdgcn_exp2f((r.tail - o.m) * c);
+      const bool tail_on = bucket && j < d.vocab && bits[j >> 5] >> (j & 31) & 1;
+      const float tail = tail_on ? -__builtin_inff() : r.tail;
+      top = max3(top, tail, tail);
+      o.raise(tail, c, rescale);
+      off += __builtin_amdgcn_exp2f((tail - o.m) * c);
       if (!GRAD && more) r.load_tail(nr, full, d.vocab);
-      if (bucket && j < d.vocab && bits[j >> 5] >> (j & 31) & 1) on += e;
-      else off += e;
-      m = block_reduce<TPB>(top, fpart[0], Max());
-      rescale(__builtin_amdgcn_exp2f((o.m - m) * c));
-      off = block_reduce<TPB>(off, fpart[1], Sum());
-      on = block_reduce<TPB>(on, fpart[2], Sum());
-      total = on + off;
+      const float listed = bucket && first ? at_idx : -__builtin_inff();
+      Pair tops = block_reduce<TPB>(Pair{top, max3(listed, LOWEST, LOWEST)}, pair[0], PairMax());
+      tops = {uniform(tops.off), uniform(tops.on)};
+      rescale(__builtin_amdgcn_exp2f((o.m - tops.off) * c));
+      const float on = __builtin_amdgcn_exp2f((listed - tops.on) * c);
+      Pair sums = block_reduce<TPB>(Pair{off, on}, pair[1], PairSum());
+      sums = {uniform(sums.off), uniform(sums.on)};
+      // (LOWEST is the maximum of no logit, and its sum 0)
+      m = Max()(tops.off, tops.on);
+      off = sums.off;
+      const float scaled_off = off * __builtin_amdgcn_exp2f((tops.off - m) * c);
+      total = scaled_off + sums.on * __builtin_amdgcn_exp2f((tops.on - m) * c);
       if (total == 0.f) m = 0.f;
       // to base 2; a row without a finite logit has q = 0 and log q = -inf
       const float log_total = total == 0.f ? 0.f : __builtin_amdgcn_logf(total);
-      const float log_off = total == 0.f ? -__builtin_inff() : __builtin_amdgcn_logf(off) - log_total;
+      const double log_q_r = off == 0.f ? -double(__builtin_inff())
+                                        : (double(tops.off) - double(m)) * double(c) +
+                                              double(__builtin_amdgcn_logf(off)) - double(log_total);
+      q_r = scaled_off / total;
+      ref = tops.off, log_ref = 0.f;
       double term = 0.0;
       if (p > 0.f) term = double(p) * ((double(log_p) - double(at_idx - m) * double(c)) + double(log_total));
       term = block_reduce<TPB>(term, dpart[1], Sum());
       if (t == 0) {
-        if (rest > 0.0) term += rest * (double(__builtin_amdgcn_logf(float(rest))) - double(log_off));
+        if (rest > 0.0) term += rest * (double(__builtin_amdgcn_logf(float(rest))) - log_q_r);
         d.loss[row] = masked(float(double(w) * d.temperature * d.temperature * LN2 * term), keep);
         if (d.stats) {
           d.stats[3 * row] = masked(m, keep);
           d.stats[3 * row + 1] = masked(total == 0.f ? -__builtin_inff() : log_total * float(LN2), keep);
-          d.stats[3 * row + 2] = masked(log_off * float(LN2), keep);
+          d.stats[3 * row + 2] = masked(float(log_q_r * LN2), keep);
         }
       }
     } else {
       m = d.stats[3 * row];
-      const float log_total = d.stats[3 * row + 1] * LOG2E, log_off = d.stats[3 * row + 2] * LOG2E;
+      const float log_total = d.stats[3 * row + 1] * LOG2E;
       total = __builtin_amdgcn_exp2f(log_total);
-      off = __builtin_amdgcn_exp2f(log_total + log_off);
+      const float log_q_r = d.stats[3 * row + 2] * LOG2E;
+      q_r = __builtin_amdgcn_exp2f(log_q_r);
+      off = log_q_r == -__builtin_inff() ? 0.f : 1.f;
+      ref = m, log_ref = log_total + log_q_r;
     }
     // ---- the gradient
     if (GRAD) {
       const double gain = double(w) * d.temperature;
       const float f_on = float(total == 0.f ? 0.0 : gain * mass / total);
-      const float f_off = rest > 0.0 && off > 0.f ? float(gain * (mass / total - rest / off)) : f_on;
+      // Off the list P q_j - r q_j / q_r is taken as (q_j / q_r) (P q_r - r): the
+      // first factor is at most 1, however small q_r.
+      float f_off = f_on;
+      if (rest > 0.0 && off > 0.f) f_off = float(gain * (mass * q_r - rest) / off);
+      else ref = m, log_ref = 0.f;
+      auto exps = [&](float x) {
+        if constexpr (LOSS) return __builtin_amdgcn_exp2f((x - ref) * c);
+        // (what the stats round off may take it past 1, by their |log q_r| 2^-24)
+        return __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(fmaf(x - ref, c, -log_ref)), 0.f, 1.f);
+      };
       r.template each<true>(lr, full, [&](int i, int ch, const float(&x)[E<T>], Raw) {
         float g[E<T>];
-        for (int e = 0; e < E<T>; ++e) g[e] = __builtin_amdgcn_exp2f((x[e] - m) * c) * f_off;
+        for (int e = 0; e < E<T>; ++e) g[e] = exps(x[e]) * f_off;
         Raw q = pack(g);
         q &= keep;
         if (ch < full) store_once(CH > 0 ? r.chunk_at(gr, i) : gr + int64_t(ch) * E<T>, q);
         if constexpr (CH > 0) r.load_chunk(i, nr, ahead);
       });
       if (full * E<T> + t < d.vocab)
-        put(gr + full * E<T> + t, masked(__builtin_amdgcn_exp2f((r.tail - m) * c) * f_off, keep));
+        put(gr + full * E<T> + t, masked(exps(r.tail) * f_off, keep));
       if (more) r.load_tail(nr, full, d.vocab);
       __syncthreads();
-      if (writes)
+      if (first)
         put(gr + idx, masked(__builtin_amdgcn_exp2f((at_idx - m) * c) * f_on - float(gain) * p_col, keep));
     } else {
       __syncthreads();

@@ -141,13 +141,20 @@ struct Row {
   // unpacks them anew (the empty asm hides that they have not changed):
   // kept from pass to pass, the unpacked row would be twice the registers.
   // ONCE: without registers for the row, this is the last pass over it.
+  // edit(chunk, it as it lies) may change elements first: for good in registers,
+  // else for this pass.
   template <bool ONCE = false, class F>
   __device__ __forceinline__ void each(const T* row, int full, F f) {
+    each<ONCE>(row, full, f, [](int, Raw&) {});
+  }
+  template <bool ONCE, class F, class G>
+  __device__ __forceinline__ void each(const T* row, int full, F f, G edit) {
     if constexpr (CH > 0) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         Raw& q = reg[i];
         asm volatile("" : "+v"(q));
+        edit(i * TPB + thread_of_row(), q);
         float x[E<T>];
         unpack(q, x);
         f(i, i * TPB + thread_of_row(), x, q);
@@ -158,7 +165,8 @@ struct Row {
       // with -inf), so that what f counts over the wave stays the same in all
       constexpr int U = V::UNROLL;
       constexpr uint32_t ni = neg_inf_word<T>();
-      auto take = [&](int at, const Raw& q) {
+      auto take = [&](int at, Raw& q) {
+        edit(at, q);
         float x[E<T>];
         unpack(q, x);
         f(0, at, x, q);

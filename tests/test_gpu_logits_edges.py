@@ -72,3 +72,90 @@ def test_log_sum_exp_of_rows_with_infinities(v, dtype):
         assert got[0] == INF and got[1] == INF and got[5] == INF and got[4] == -INF
         assert np.isnan(got[2]) and np.isnan(got[3])
         assert abs(got[6] - wl[6]) <= 4e-5 + 2.0 ** -22 * abs(wl[6])
+
+
+def _close(got, want, tol, dtype):
+    got = got.astype(np.float64)
+    lo, hi = want - tol - 1e-38, want + tol + 1e-38
+    if dtype == "bf16":
+        lo, hi = bf16(lo), bf16(hi)
+    bad = ~((lo <= got) & (got <= hi))
+    assert not bad.any(), (np.argwhere(bad)[:3], got[bad][:5], want[bad][:5],
+                           np.broadcast_to(tol, got.shape)[bad][:5])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("v,k,temperature", [(50, 1, 1.0), (50, 7, 0.05), (1000, 8, 0.5), (6001, 30, 1.0),
+                                             (20000, 64, 2.0), (60001, 200, 0.3), (140001, 16, 1.0)])
+def test_mass_off_the_list_far_below_the_largest_logit(v, k, temperature, dtype):
+    """All columns off the list lie a gap below those on it, from a few T to the
+    masks that models write (-1e4): q_r down to e^-5000 and further. The bounds of
+    the other tests, the mass off the list (and its error) taken as each column's
+    share of it; from stats the fp32 log q_r and what is made of it round by at most
+    2^-21 of |log q_r| of the remainder's term."""
+    T = temperature
+    print(f"[distill gap] {v} k {k} T {T} {dtype}", flush=True)
+    gaps = np.array([3.0, 60.0, 80.0, 86.0, 88.0, 95.0, 104.0, 300.0, 5000.0])
+    rests = np.array([1e-3, 0.3, 0.02])
+    n = len(gaps) * len(rests)
+    gap, r = np.repeat(gaps, 3), np.tile(rests, 3 * 3)
+    rng = np.random.default_rng(v)
+    s = rng.normal(0, 1, (n, v)) * T - (gap * T)[:, None] / 2
+    idx = np.array([rng.choice(v, k, replace=False) for _ in range(n)])
+    np.put_along_axis(s, idx, rng.normal(0, 1, (n, k)) * T + (gap * T)[:, None] / 2, 1)
+    p = rng.random((n, k)) + 0.1
+    p *= ((1 - r) / p.sum(1))[:, None]
+    st = torch.tensor(s, dtype=torch.float32, device="cuda").to(getattr(torch, DT[dtype]))
+    val = torch.tensor(T * np.log(p), dtype=torch.float32, device="cuda")
+    ix = torch.tensor(idx, dtype=torch.int32, device="cuda")
+    lse = torch.zeros(n, device="cuda")
+    w = torch.tensor(rng.random(n) + 0.5, dtype=torch.float32, device="cuda")
+    loss, grad, stats = head.distill(_np(st), host(val), idx, host(lse), T, host(w).astype(np.float64))
+    assert np.isfinite(loss).all() and stats[:, 2].min() < -4900
+    wn, sn = host(w).astype(np.float64), _np(st).astype(np.float64)
+    q = np.exp((sn - stats[:, :1]) / T - stats[:, 1:2])
+    on = np.zeros((n, v), bool)
+    np.put_along_axis(on, idx, True, 1)
+    m_off = np.where(on, -np.inf, sn).max(1, keepdims=True)
+    share = np.where(on, 0.0, np.exp((np.where(on, m_off, sn) - m_off) / T))
+    share /= share.sum(1, keepdims=True)
+    pd = np.zeros((n, v))
+    np.put_along_axis(pd, idx, p, 1)
+    ltol = wn * T ** 2 * (1e-4 + 2.0 ** -21 * np.abs(sn).max(1) / T)
+    gtol = (wn * T)[:, None] * 1e-4 * (q + share + pd)
+    kw = dict(t_lse=lse, temperature=T)
+    got, gstats = kq.kq_distill_loss(st, val, ix, weight=w, **kw)
+    _close(host(got), loss, ltol, "f32")
+    np.testing.assert_allclose(host(gstats)[:, 2], stats[:, 2], rtol=2.0 ** -21, atol=1e-4)
+    l2, g2 = kq.kq_distill_loss_grad(st, val, ix, weight=w, **kw)
+    _close(host(l2), loss, ltol, "f32")
+    _close(_np(g2), grad, gtol, dtype)
+    from_stats = (wn * T * r * np.abs(stats[:, 2]))[:, None] * 2.0 ** -21 * share
+    for at in (host(gstats), stats.astype(np.float32)):
+        g3 = kq.kq_distill_grad(st, val, ix, torch.tensor(at, device="cuda"), w, **kw)
+        _close(_np(g3), grad, gtol + from_stats, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_lists_that_hold_every_column_a_mask_leaves(dtype):
+    """Off the list there is the type's lowest value, or -inf, and nothing else:
+    a loss of r / T times that distance (or +inf), and a gradient without NaN."""
+    dt = getattr(torch, DT[dtype])
+    s = torch.full((2, 700), torch.finfo(dt).min, dtype=dt, device="cuda")
+    s[1] = -INF
+    s[:, :4] = torch.tensor([1.0, 2.0, -3.0, 0.5], device="cuda").to(dt)
+    idx = torch.tensor([[0, 1, 2, 3]] * 2, dtype=torch.int32, device="cuda")
+    val = torch.log(torch.full((2, 4), 0.2, device="cuda"))
+    lse = torch.zeros(2, device="cuda")
+    loss, grad = kq.kq_distill_loss_grad(s, val, idx, t_lse=lse)
+    loss2, stats = kq.kq_distill_loss(s, val, idx, t_lse=lse)
+    want = 0.2 * -float(torch.finfo(dt).min)
+    assert abs(loss[0].item() / want - 1) < 1e-5 and loss[1].item() == INF
+    assert torch.equal(loss, loss2)
+    g3 = kq.kq_distill_grad(s, val, idx, stats, torch.ones(2, device="cuda"), t_lse=lse)
+    _, wg, _ = head.distill(_np(s), host(val), host(idx), host(lse), 1.0)
+    for g in (grad, g3):
+        assert not torch.isnan(g).any()
+        assert np.all(np.abs(_np(g)[:, :4] - wg[:, :4]) <= 2.0 ** -8 * np.abs(wg[:, :4]) + 1e-4)
+    tol = 1e-4 + (2.0 ** -8 * np.abs(wg[0]) if dtype == "bf16" else 0)
+    assert np.all(np.abs(_np(grad)[0] - wg[0]) <= tol)
