@@ -461,7 +461,8 @@ kq_status kq_linear_i8(const void* x, kq_dtype dt, int64_t ldx, float clip, cons
  * index; a NaN counts as larger than any number, +0 and -0 as equal):
  *   values  n x k floats;  index  n x k int32
  *   lse     n floats: log sum_j exp(logits_j / T) over the whole row, or NULL
- *           (+inf where a logit is +inf and none is NaN)
+ *           (+inf where a logit is +inf and none is NaN); the quotients of the
+ *           listed logits are taken as kq_distill_loss rounds them
  * k <= vocab <= 2^30. */
 kq_status kq_top_logits(const void* logits, kq_dtype dt, int64_t n, int64_t vocab, int64_t ld,
                         int32_t k, float temperature, float* values, int32_t* index, float* lse,
@@ -470,7 +471,8 @@ kq_status kq_top_logits(const void* logits, kq_dtype dt, int64_t n, int64_t voca
 /* With q = softmax(s / T) of the student's logits s and the teacher's list
  * (t_values, t_index: n x k, the logits and columns of kq_top_logits):
  *   t_lse NULL:  p = softmax of the list's t / T;  r = 0
- *   t_lse given: p_k = exp(t_k / T - t_lse);  r = 1 - sum_k p_k is the
+ *   t_lse given: p_k = exp(t_k / T - t_lse), t_k / T being t_k times the
+ *                reciprocal of T, each in fp32;  r = 1 - sum_k p_k is the
  *                teacher's mass off the list, against the student's q_r = sum
  *                of q off the list (r <= 2^-16 counts as 0: t_lse is fp32)
  *   loss    = w T^2 [ sum_k p_k (log p_k - log q_k) + r (log r - log q_r) ]

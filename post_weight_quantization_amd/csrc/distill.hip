@@ -126,11 +126,11 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
     double mass = 1.0, rest = 0.0;
     float log_p;  // to base 2
     if (bucket) {
-      // t / T rounds by itself, as it did in the sum that Z is the logarithm of:
-      // of a list that holds almost all of it, the rounding is then in both and
-      // goes off (Z's own is left). In one operation with Z it would stay in p
-      // alone, up to 2e-6 at t / T = 50, and 1 - sum p, which counts from 2^-16
-      // on, would be off by as much.
+      // t / T rounds by itself, as in the log-sum-exp that top logits come with: of a
+      // list that holds almost all of it, the rounding is then in both and goes off
+      // (Z's own is left). In one operation with Z it would stay in p alone, up to
+      // 2e-6 at t / T = 50, and 1 - sum p, which counts from 2^-16 on, would be off by
+      // as much.
       float scaled = tv * inv_t;
       asm volatile("" : "+v"(scaled));
       log_p = (scaled - d.t_lse[row]) * LOG2E;

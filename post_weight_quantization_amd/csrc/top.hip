@@ -23,6 +23,11 @@
 // leaves few columns. What that does not settle (and a row with a NaN or +inf)
 // is searched bit by bit for the K-th largest key, counting.
 //
+// The log-sum-exp is that of the quotients l / T as the distillation rounds
+// them: of a list with nearly all of the mass, what it leaves is a difference of
+// numbers that both round alike (T = 0.7, l / T near 60: within 2e-6, else up to
+// 4e-6). Only listed logits are corrected for it; the others' mass is then small.
+//
 // 64 of 4096 x 128256 bf16 take 206 us, 5.1 TB/s; vector instructions bound it:
 // they keep the SIMDs busy 83 % of the time, half of that an exponential per
 // element, at a quarter of the rate of the others. One row alone takes its CU 13
@@ -60,6 +65,15 @@ __device__ inline int lanes_below(uint64_t mask) {
   return __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(mask), 0));
 }
 
+// v / T as the distillation takes it, v times 1 / T rounded to fp32, and what
+// that is above the exact product
+__device__ inline float quotient(float v, float inv_t) {
+  float z = v * inv_t;
+  asm volatile("" : "+v"(z));  // (by itself, not within a sum)
+  return z;
+}
+__device__ inline float quotient_error(float v, float inv_t) { return -fmaf(v, inv_t, -quotient(v, inv_t)); }
+
 template <int NW>
 struct TopLds {
   __align__(16) uint64_t list[LIST + 2];
@@ -69,6 +83,7 @@ struct TopLds {
   __align__(16) uint16_t group[GROUPS];
   int pivots[2][16];
   float part[NW];
+  float shift[K_MAX];
   float sums[NW];  // apart from `part`, which a wave may still read when another is done with the row
   int ipart[2][NW];
   int count, overflow;
@@ -137,6 +152,7 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int full = vocab / E<T>;
   const float c = inv_t * 1.44269504088896340736f;
+  const bool inexact = lse && (__float_as_uint(inv_t) & 0x7fffffu) != 0;
   Row<T, V> r;
   r.load(logits + int64_t(blockIdx.x) * ld, full, vocab);
   for (int row = blockIdx.x; row < n; row += gridDim.x) {
@@ -257,11 +273,15 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
       append(i < items && v >= tau, v, s.chunk_no[w][at] * E<T> + e);
     }
     sum = block_reduce<TPB>(sum, s.sums, Sum());
-    // (no finite logit: the sum is 0; NaN: the row's largest, found below, is the
-    // answer)
-    if (lse && t == 0 && sum == sum) {
-      const float shift = fmaf(-m, scale, ref) * 0.69314718055994530942f;
-      lse[row] = sum == 0.f ? -__builtin_inff() : m * inv_t + (logf(sum) + shift);
+    // the log-sum-exp, where no quotient rounds (1 / T a power of 2) or it is not a
+    // finite number (no finite logit: the sum is 0; NaN: the row's largest, found
+    // below, is the answer; a quotient past fp32 is the answer), else less what the
+    // listed quotients' rounding moves it by
+    const bool rounds = inexact && sum > 0.f && fabsf(m * inv_t) < __builtin_inff();
+    float rel = 0.f;  // of the row against its largest
+    if (lse && w == 0 && sum == sum) {
+      rel = logf(sum) + fmaf(-m, scale, ref) * 0.69314718055994530942f;
+      if (lane == 0 && !rounds) lse[row] = sum == 0.f ? -__builtin_inff() : m * inv_t + rel;
     }
     int count = s.count;
     if (s.overflow || count > LIST || sum != sum) {
@@ -302,10 +322,21 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
         const float v = value_of(uint32_t(s.list[i] >> 32));
         values[int64_t(row) * k + at] = v;
         if (at == 0 && lse && sum != sum) lse[row] = v;  // +inf, or NaN, which is above it
+        if (rounds) {  // to first order: the entry's share times the rounding
+          const float share = __builtin_amdgcn_exp2f(fmaf(v, scale, -ref)) / sum;
+          s.shift[at] = share > 0.f ? share * quotient_error(v, inv_t) : 0.f;
+        }
         index[int64_t(row) * k + at] = int32_t(~uint32_t(s.list[i]));
       }
     }
     __syncthreads();
+    // (the first wave; s.shift is written again several barriers later)
+    if (rounds && w == 0) {
+      float moved = 0.f;
+      for (int i = lane; i < k; i += 64) moved += s.shift[i];
+      moved = wave_reduce(moved, Sum()) - quotient_error(m, inv_t);
+      if (lane == 0) lse[row] = quotient(m, inv_t) + (rel + moved);
+    }
   }
 }
 

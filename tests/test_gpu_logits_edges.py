@@ -159,3 +159,32 @@ def test_lists_that_hold_every_column_a_mask_leaves(dtype):
         assert np.all(np.abs(_np(g)[:, :4] - wg[:, :4]) <= 2.0 ** -8 * np.abs(wg[:, :4]) + 1e-4)
     tol = 1e-4 + (2.0 ** -8 * np.abs(wg[0]) if dtype == "bf16" else 0)
     assert np.all(np.abs(_np(grad)[0] - wg[0]) <= tol)
+
+
+@pytest.mark.parametrize("temperature", [0.7, 1.5, 3.0, 1.0])
+@pytest.mark.parametrize("k", [1, 4])
+def test_rest_of_the_librarys_own_lists(k, temperature):
+    """A teacher's k logits hold all but r = 3e-5 to 1e-3, at l / T of 40 to 62 where
+    fp32 steps are 3.8e-6, and list and log-sum-exp come from kq_top_logits. With
+    the student equal to the teacher the gradient off the list adds up to
+    T (q_r - r'), r' what the list leaves by p and log-sum-exp, q_r the mass
+    itself. Bound: half a step of the log-sum-exp, 1.91e-6; of p's exponentials and
+    arguments 2^-23 and 2^-24 log2(e) 3, of the sum's 2^-23 and 2^-24 2, each of 1:
+    9e-7; r's own 1e-4 of itself."""
+    n, v = 4000, 600
+    T = float(np.float32(temperature))
+    rng = np.random.default_rng(k)
+    x = rng.normal(0, 1, (n, v))
+    x[:, :k] = rng.uniform(-1.5, 0.0, (n, k))
+    r = np.geomspace(3e-5, 1e-3, n)
+    x[:, k:] += (np.log(r * np.exp(x[:, :k]).sum(1)) - np.log(np.exp(x[:, k:]).sum(1)))[:, None]
+    x += rng.uniform(42, 60, (n, 1))
+    teacher = torch.tensor(x * T, dtype=torch.float32, device="cuda")
+    val, idx, lse = kq.kq_top_logits(teacher, k, temperature)
+    assert torch.equal(idx.sort(1).values, torch.arange(k, dtype=torch.int32, device="cuda").expand(n, k))
+    assert lse.max() < 64
+    _, grad = kq.kq_distill_loss_grad(teacher, val, idx, t_lse=lse, temperature=temperature)
+    z = teacher.double() / T
+    rest = torch.exp(torch.logsumexp(z[:, k:], 1) - torch.logsumexp(z, 1))
+    err = (grad[:, k:].double().sum(1) / T).abs() - 1e-4 * rest
+    assert err.max().item() <= 1.91e-6 + 9e-7, err.max().item()
