@@ -183,8 +183,15 @@ __global__ __launch_bounds__(256) void pack_i8_kernel(const uint8_t* __restrict_
   if (threadIdx.x == 0) zero_out[row] = zero[row] - 128.f;
 }
 
-// y of one sum (see the top of the file): the conversion of the exact sum, the
-// two scales and the bias each round once
+// y of one exact sum (see the top of the file), the same bits whichever kernel
+// made the sum: its conversion, the two scales and the bias each round once, and
+// none of them is joined with another. No bias: -0, which changes nothing.
+constexpr float NO_BIAS = -0.f;
+__device__ __forceinline__ float i8_value(int sum, float a_scale, float w_scale, float bias) {
+#pragma clang fp contract(off)
+  return float(sum) * a_scale * w_scale + bias;
+}
+
 struct I8Epi {
   const float* a_scale;
   const int32_t* a_sum;
@@ -196,8 +203,7 @@ struct I8Epi {
   template <class Y>
   __device__ __forceinline__ void put(int sum, int64_t t, int64_t o, Y* y) const {
     if (w_zero) sum -= int(rintf(w_zero[o])) * a_sum[t];
-    const float f = float(sum) * a_scale[t] * w_scale[o];
-    store_y(y + t * ldy + o, bias ? f + bias[o] : f);
+    store_y(y + t * ldy + o, i8_value(sum, a_scale[t], w_scale[o], bias ? bias[o] : NO_BIAS));
   }
 };
 
@@ -259,8 +265,7 @@ struct I8Tile {
 // y from the sums of a wave's tiles: 32 tokens at a time go through LDS as
 // they are, so that a lane then has the same few channels of token after
 // token, with their scales in registers, and a wave writes whole runs of a
-// token's channels. The fp32 conversion of the sum, the two scales and the
-// bias each round once; y is rounded to its type after that. Nothing is loaded
+// token's channels. Nothing is loaded
 // within the passes (with the tokens' scales read there, and the sums rounded
 // in software, a tile of 256 x 192 took 29000 cycles, now 19000), and y goes past
 // the caches' usual order (14000: what 256 CUs write at once takes memory 11000).
@@ -290,7 +295,7 @@ __device__ inline void i8_store(const v16i (&acc)[MI][NJ], const I8Epi& e, int64
     const int64_t oc = min(o + k, e.m - 1);
     ws[k] = e.w_scale[oc];
     wz[k] = e.w_zero ? int(rintf(e.w_zero[oc])) : 0;
-    bias[k] = e.bias ? e.bias[oc] : 0.f;
+    bias[k] = e.bias ? e.bias[oc] : NO_BIAS;
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
@@ -324,7 +329,7 @@ __device__ inline void i8_store(const v16i (&acc)[MI][NJ], const I8Epi& e, int64
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
           // (both factors have 24 bits)
-          store_y(v + k, float(src[k / 4][k % 4] - __mul24(wz[k], sum)) * a * ws[k] + bias[k]);
+          store_y(v + k, i8_value(src[k / 4][k % 4] - __mul24(wz[k], sum), a, ws[k], bias[k]));
         }
         Y* dst = y + tk * e.ldy + o;
         if (o + CH <= e.m) {
