@@ -31,6 +31,11 @@ import torch
 from . import api
 
 
+def _without_gradient(name, t):
+    if t is not None and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: expected a tensor that needs no gradient (none is computed for it)")
+
+
 @dataclass
 class I8Linear:
     """y = x W^T + b in 8-bit integers (see kq_linear_i8)."""
@@ -62,7 +67,9 @@ class I8Linear:
 
     def __call__(self, x, dtype=None):
         """x: (..., d_in) bf16 or fp32; returns (..., d_out) of x's type, or of
-        ``dtype``. Not differentiable."""
+        ``dtype``. Not differentiable: x must not need a gradient, which would be
+        lost here (detach it, or call under torch.no_grad())."""
+        _without_gradient("x", x)
         y = api.kq_linear_i8(x.detach().reshape(-1, self.d_in), self.codes, self.scale, w_zero=self.zero,
                              bias=self.bias, dtype=dtype)
         return y.reshape(*x.shape[:-1], self.d_out)
