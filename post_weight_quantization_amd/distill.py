@@ -95,28 +95,33 @@ def teacher_top(logits, k: int, temperature: float = 1.0, rest: bool = True) -> 
 
 class _Distill(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, teacher, weight):
-        loss, stats = api.kq_distill_loss(logits, teacher.values, teacher.index, teacher.lse, teacher.temperature,
-                                          weight)
-        ctx.teacher = teacher
-        ctx.save_for_backward(logits, stats, weight)
+    def forward(ctx, logits, weight, values, index, lse, temperature):
+        loss, stats = api.kq_distill_loss(logits, values, index, lse, temperature, weight)
+        ctx.temperature = temperature
+        # (all of them, so that torch notices one that was written in between)
+        ctx.save_for_backward(logits, weight, values, index, lse, stats)
         return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dloss):
-        logits, stats, weight = ctx.saved_tensors
-        t = ctx.teacher
+        logits, weight, values, index, lse, stats = ctx.saved_tensors
         d = (dloss.float() if weight is None else dloss.float() * weight).contiguous()
-        return api.kq_distill_grad(logits, t.values, t.index, stats, d, t.lse, t.temperature), None, None
+        grad = api.kq_distill_grad(logits, values, index, stats, d, lse, ctx.temperature)
+        return grad, None, None, None, None, None
 
 
 def distill_loss(logits, teacher: TeacherTop, weight=None):
     """The loss of each token of logits (..., vocab; bf16 or fp32) against the
     teacher's answers, fp32, differentiable in logits. weight: fp32, one a
-    token (0: a token that does not count, whatever its logits hold)."""
-    loss = _Distill.apply(logits.reshape(-1, logits.shape[-1]), teacher,
-                          None if weight is None else weight.reshape(-1).contiguous())
+    token (0: a token that does not count, whatever its logits hold). Neither
+    the weights nor the answers may need a gradient, or be written before backward.
+    """
+    for name, t in (("weight", weight), ("values", teacher.values), ("lse", teacher.lse)):
+        _without_gradient(name, t)
+    loss = _Distill.apply(logits.reshape(-1, logits.shape[-1]),
+                          None if weight is None else weight.reshape(-1).contiguous(), teacher.values,
+                          teacher.index, teacher.lse, teacher.temperature)
     return loss.reshape(logits.shape[:-1])
 
 

@@ -20,3 +20,15 @@ def test_the_8_bit_layer_refuses_to_lose_a_gradient():
         _layer()(x)
     with pytest.raises(ValueError, match="GPU"):
         _layer()(x.detach())
+
+
+@pytest.mark.parametrize("which", ["weight", "values", "lse"])
+def test_the_loss_refuses_gradients_it_does_not_compute(which):
+    t = dict(weight=torch.ones(4), values=torch.zeros(4, 2), lse=torch.zeros(4))
+    t[which].requires_grad_()
+    teacher = distill.TeacherTop(t["values"], torch.zeros(4, 2, dtype=torch.int32), t["lse"])
+    logits = torch.zeros(4, 9, requires_grad=True)
+    with pytest.raises(ValueError, match=f"^{which}: expected a tensor that needs no gradient"):
+        distill.distill_loss(logits, teacher, t["weight"])
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+        distill.distill_loss(logits, teacher, t["weight"])
