@@ -18,9 +18,11 @@
 //      value, complement of its index), so no two are equal, and its rank is the
 //      number of larger keys on the list.
 // Should either overflow (128 chunks of a wave, 1024 elements: many equal
-// logits), a second pass takes what is above tau and, of the first K columns,
-// what equals it: enough where that makes K of them, as in a row whose mask
-// leaves few columns. What that does not settle (and a row with a NaN or +inf)
+// logits), a second pass takes what is above the largest key that begins like
+// tau's, and of the first K columns what equals it: enough where that makes K
+// of them, as in a row whose mask, of whatever value, leaves few columns (256 x
+// 100000 with 5 left: 71 us bf16, 128 fp32; searched, 1770 and 3370).
+// What that does not settle (and a row with a NaN or +inf)
 // is searched bit by bit for the K-th largest key, counting.
 //
 // The log-sum-exp is that of the quotients l / T as the distillation rounds
@@ -164,6 +166,15 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
     float g[GP];
     for (int i = 0; i < GP; ++i) g[i] = -__builtin_inff();
     r.each(lr, full, [&](int i, int, const float(&x)[E<T>], Raw) {
+      // Rows of a chunk a thread or less: a group for every two elements, for
+      // there may be fewer chunks than K (of up to 1024 elements all may go on
+      // the list).
+      if constexpr (E<T> == 8 && CH == 4 && GP == 4) {
+        if (i == 0 && full <= TPB) {
+          for (int e = 0; e < GP; ++e) g[e] = max3(x[2 * e], x[2 * e + 1], x[2 * e + 1]);
+          return;
+        }
+      }
       const float top = max_of(x);
       g[i % GP] = max3(g[i % GP], top, top);
     });
@@ -286,11 +297,23 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
     int count = s.count;
     if (s.overflow || count > LIST || sum != sum) {
       __syncthreads();
-      if (t == 0) s.count = 0;
-      __syncthreads();
-      gather<T, TPB>(lr, vocab, s, [&](float v, int j) { return v > tau || (v == tau && j < k); });
-      __syncthreads();
-      count = s.count;
+      if (sum == sum) {
+        if (t == 0) s.count = 0;
+        __syncthreads();
+        uint32_t most = 0;
+        gather<T, TPB>(lr, vocab, s, [&](float v, int) {
+          const uint32_t q = key_of(v);
+          if (q >> 16 == key) most = max(most, q);
+          return q >> 16 > key;
+        });
+        most = block_reduce<TPB>(most, reinterpret_cast<uint32_t*>(s.ipart[0]), Max());
+        if (t < k && key_of(to_f32(lr[t])) == most) {
+          const int at = atomicAdd(&s.count, 1);
+          if (at < LIST) s.list[at] = entry_of(to_f32(lr[t]), t);
+        }
+        __syncthreads();
+        count = s.count;
+      }
       if (count > LIST || count < k || sum != sum) {
         search<T, TPB>(lr, vocab, k, s);
         count = s.count;

@@ -188,3 +188,61 @@ def test_rest_of_the_librarys_own_lists(k, temperature):
     rest = torch.exp(torch.logsumexp(z[:, k:], 1) - torch.logsumexp(z, 1))
     err = (grad[:, k:].double().sum(1) / T).abs() - 1e-4 * rest
     assert err.max().item() <= 1.91e-6 + 9e-7, err.max().item()
+
+
+def _time(logits, k):
+    """us a call, the least of several."""
+    best = INF
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(3):
+            kq.kq_top_logits(logits, k)
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) / 3e-3)
+    return best
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masks_of_any_value_cost_alike(dtype):
+    """Five columns left, the rest one value: whatever that value, the row is
+    settled by the pass that -inf takes (else it is searched bit by bit, some 64
+    passes, over ten times as long)."""
+    dt = getattr(torch, DT[dtype])
+    n, v, k = 256, 100000, 20
+    left = _np(torch.randn(n, 5, device="cuda").to(dt))
+    times = {}
+    for mask in (-INF, torch.finfo(dt).min, -1e4, -1.0, 0.25, 7.0):
+        t = torch.full((n, v), mask, dtype=dt, device="cuda")
+        at = [3, 700, 40000, 70001, v - 1]
+        t[:, at] = torch.tensor(left, device="cuda").to(dt) + (16.0 if mask > -100 else 0.0)
+        values, index, _ = kq.kq_top_logits(t, k)
+        wv, wi, _ = head.top_logits(_np(t[:2]), k)
+        np.testing.assert_array_equal(host(index[:2]), wi)
+        np.testing.assert_array_equal(host(values[:2]), wv.astype(np.float32))
+        times[mask] = _time(t, k)
+    print(times)
+    assert all(times[m] <= 4 * times[-INF] for m in times), times
+
+
+def test_short_rows_with_long_lists():
+    """Fewer 16-byte chunks than K: rows of 1025 to 2047 bfloat16, lists of up to
+    256. Right at every length, and not searched bit by bit."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for v in (1025, 1500, 1777, 2047, 2055, 2056, 2064):
+        t = torch.randn(300, v, device="cuda", generator=g).to(torch.bfloat16)
+        t[0] = -INF
+        t[1, 7:] = -INF
+        t[2] = 1.5
+        t[3, 200:] = -2.0
+        for k in (129, 200, 256):
+            values, index, _ = kq.kq_top_logits(t, k)
+            wv, wi, _ = head.top_logits(_np(t[:40]), k)
+            np.testing.assert_array_equal(host(index[:40]), wi)
+            np.testing.assert_array_equal(host(values[:40]), wv.astype(np.float32))
+    rows = torch.randn(4096, 1500, device="cuda", generator=g).to(torch.bfloat16)
+    # (lists of 200 take more ranking than lists of 64, not ten times as long)
+    short, long_ = _time(rows, 64), _time(rows, 200)
+    print(short, long_)
+    assert long_ <= 4 * short, (short, long_)
