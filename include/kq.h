@@ -478,11 +478,11 @@ kq_status kq_top_logits(const void* logits, kq_dtype dt, int64_t n, int64_t voca
  *   loss    = w T^2 [ sum_k p_k (log p_k - log q_k) + r (log r - log q_r) ]
  *   dloss/ds_j = w T [ c_j q_j - p_j ],  c_j = P on the list and P - r / q_r
  *                off it, P = sum_k p_k + r
- *   weight  n floats w (a row of weight 0 gets loss and gradient 0, and its
- *           logits are not looked at), or NULL for ones
+ *   weight  n floats w (a row of weight 0 gets loss and gradient 0 whatever its
+ *           logits hold), or NULL for ones
  *   loss    n floats
  *   stats   n x 3 floats for kq_distill_grad: the largest logit m,
- *           log sum exp((s - m) / T), log q_r; or NULL
+ *           log sum exp((s - m) / T), log q_r, whatever the weight; or NULL
  * An entry whose index is below 0 or at least vocab is none (lists may have
  * fewer than k entries, or none); entries of the same index add up. A row
  * whose logits are all -inf has q = 0. vocab <= 524288. */

@@ -76,8 +76,6 @@ def distill(logits, values, index, t_lse=None, temperature=1.0, weight=None):
     with np.errstate(divide="ignore", invalid="ignore"):
         for i in range(n):
             w = 1.0 if weight is None else float(weight[i])
-            if w == 0.0:
-                continue
             m = np.max(s[i])
             if m == -np.inf:
                 log_q, q, log_sum = np.full(v, -np.inf), np.zeros(v), -np.inf
@@ -113,6 +111,8 @@ def distill(logits, values, index, t_lse=None, temperature=1.0, weight=None):
                 log_q_off = (m_off - m) / T + np.log(np.sum(e_off)) - log_sum
                 share = e_off / np.sum(e_off)  # q_j / q_r
             stats[i] = m, log_sum, log_q_off
+            if w == 0.0:
+                continue
             value = 0.0
             for (j, _), lp in zip(entries, log_p):
                 p = np.exp(lp)

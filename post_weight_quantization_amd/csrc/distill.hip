@@ -240,9 +240,11 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
         if (rest > 0.0) term += rest * (double(__builtin_amdgcn_logf(float(rest))) - log_q_r);
         d.loss[row] = masked(float(double(w) * d.temperature * d.temperature * LN2 * term), keep);
         if (d.stats) {
-          d.stats[3 * row] = masked(m, keep);
-          d.stats[3 * row + 1] = masked(total == 0.f ? -__builtin_inff() : log_total * float(LN2), keep);
-          d.stats[3 * row + 2] = masked(float(log_q_r * LN2), keep);
+          // (of the logits alone: a row without weight here may have some in
+          // the backward pass)
+          d.stats[3 * row] = m;
+          d.stats[3 * row + 1] = total == 0.f ? -__builtin_inff() : log_total * float(LN2);
+          d.stats[3 * row + 2] = float(log_q_r * LN2);
         }
       }
     } else {

@@ -246,3 +246,26 @@ def test_short_rows_with_long_lists():
     short, long_ = _time(rows, 64), _time(rows, 200)
     print(short, long_)
     assert long_ <= 4 * short, (short, long_)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rest", [False, True])
+def test_stats_of_rows_without_weight(rest, dtype):
+    """Stats are of the logits alone: a row that had no weight in the forward pass
+    gets its gradient from them like any other, and none where the gradient of
+    its loss is 0, whatever it holds."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    teacher = torch.randn(6, 5000, device="cuda", generator=g) * 3
+    s = (teacher + torch.randn(6, 5000, device="cuda", generator=g)).to(getattr(torch, DT[dtype]))
+    val, idx, lse = kq.kq_top_logits(teacher, 12)
+    kw = dict(t_lse=lse if rest else None)
+    weight = torch.tensor([0.0, 1.0, 0.0, 0.5, 0.0, 0.0], device="cuda")
+    s[5, 77] = float("nan")
+    loss, stats = kq.kq_distill_loss(s, val, idx, weight=weight, **kw)
+    assert (loss[weight == 0] == 0).all()
+    _, every = kq.kq_distill_loss(s, val, idx, **kw)
+    assert torch.equal(stats[:5], every[:5])
+    up = torch.tensor([1.0, 2.0, 0.25, 1.0, 0.0, 0.0], device="cuda")
+    grad = kq.kq_distill_grad(s, val, idx, stats, up, **kw)
+    assert torch.equal(grad[:5], kq.kq_distill_grad(s, val, idx, every, up, **kw)[:5])
+    assert grad[0].any() and grad[2].any() and not grad[4:].any()

@@ -36,3 +36,13 @@ def test_mass_far_below_the_largest_logit():
         g_off = w * T * (q_off - r * np.array([1.0, e]) / (1.0 + e))
         assert np.all(np.abs(grad[0, 1:] - g_off) <= 1e-12)
         assert abs(grad.sum()) <= 1e-12
+
+
+def test_stats_do_not_go_by_the_weight():
+    rng = np.random.default_rng(2)
+    s = rng.normal(0, 2, (3, 20))
+    val, idx, lse = head.top_logits(s + rng.normal(0, 1, s.shape), 4)
+    a = head.distill(s, val, idx, lse, 1.0, np.array([0.0, 1.0, 0.5]))
+    b = head.distill(s, val, idx, lse, 1.0)
+    np.testing.assert_array_equal(a[2], b[2])
+    assert a[0][0] == 0 and not a[1][0].any() and b[0][0] != 0
