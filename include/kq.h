@@ -455,7 +455,8 @@ kq_status kq_linear_i8(const void* x, kq_dtype dt, int64_t ldx, float clip, cons
  * Logits are n x vocab, KQ_BF16 or KQ_F32, with row stride ld >= vocab (in
  * elements) and the alignment of their element type. n may be 0: nothing is
  * launched, and the pointers are not looked at. n <= 1048576, 1 <= k <= 256,
- * temperature T finite and > 0. Asynchronous, no workspace. */
+ * temperature T finite and at least 2^-126 (the smallest normal number).
+ * Asynchronous, no workspace. */
 
 /* The k largest logits of each row in descending order (equal ones by lowest
  * index; a NaN counts as larger than any number, +0 and -0 as equal):

@@ -2,6 +2,7 @@
 // loss: argument validation on the host, then the kernels on the caller's
 // stream.
 #include <cmath>
+#include <limits>
 
 #include "kq_internal.h"
 
@@ -48,8 +49,9 @@ kq_status check_logits(kq_dtype dt, int64_t n, int64_t vocab, int64_t ld, int32_
   if (n < 0 || n > ROWS_MAX) return fail(KQ_ERR_SHAPE, "%s: 0 <= n <= 1048576", who);
   if (vocab < 1 || ld < vocab) return fail(KQ_ERR_SHAPE, "%s: 1 <= vocab <= ld", who);
   if (k < 1 || k > logits_max_k()) return fail(KQ_ERR_SHAPE, "%s: 1 <= k <= %d", who, logits_max_k());
-  if (!(std::isfinite(temperature) && temperature > 0.f))
-    return fail(KQ_ERR_ARG, "%s: temperature must be finite and > 0", who);
+  // (the reciprocal of a smaller number may be infinite)
+  if (!(std::isfinite(temperature) && temperature >= std::numeric_limits<float>::min()))
+    return fail(KQ_ERR_ARG, "%s: temperature must be finite and at least 2^-126", who);
   return KQ_OK;
 }
 

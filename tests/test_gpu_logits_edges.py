@@ -269,3 +269,27 @@ def test_stats_of_rows_without_weight(rest, dtype):
     grad = kq.kq_distill_grad(s, val, idx, stats, up, **kw)
     assert torch.equal(grad[:5], kq.kq_distill_grad(s, val, idx, every, up, **kw)[:5])
     assert grad[0].any() and grad[2].any() and not grad[4:].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", [2.0 ** -126, 1e-30, 1e30, 3e38])
+def test_the_ends_of_the_temperatures(temperature, dtype):
+    """The smallest makes softmax a choice of the largest, the greatest makes it
+    uniform; nothing is NaN. (Largest logit 0, twice: other log-sum-exps are past
+    fp32 at the smallest.)"""
+    z = torch.full((3, 3001), -2.0, device="cuda")
+    z[:, 5], z[:, 2000], z[:, 9] = 0.0, 0.0, -1.0
+    z[2, 9] = -INF
+    z = z.to(getattr(torch, DT[dtype]))
+    values, index, lse = kq.kq_top_logits(z, 3, temperature)
+    assert values[0].tolist() == [0.0, 0.0, -1.0] and index[0].tolist() == [5, 2000, 9]
+    counts = torch.tensor([2.0, 2.0, 2.0] if temperature < 1 else [3001.0, 3001.0, 3000.0], device="cuda")
+    assert ((lse - counts.log()).abs() <= 4e-5).all()
+    loss, grad = kq.kq_distill_loss_grad(z, values, index, t_lse=lse, temperature=temperature)
+    got, stats = kq.kq_distill_loss(z, values, index, t_lse=lse, temperature=temperature)
+    g3 = kq.kq_distill_grad(z, values, index, stats, torch.ones(3, device="cuda"), t_lse=lse,
+                            temperature=temperature)
+    # the student is the teacher: every term is 0 to its rounding
+    for t in (grad, g3):
+        assert not torch.isnan(t).any() and (t.float().abs() <= 2e-4 * temperature).all()
+    assert not torch.isnan(loss).any() and torch.equal(loss, got)

@@ -1,0 +1,39 @@
+"""Further argument checks of the top logits, the distillation loss and the 8-bit
+product (CPU): rejected on the host, before any launch."""
+import pytest
+
+N = pytest.importorskip("post_weight_quantization_amd._native")
+
+
+def _gpu_present():
+    try:
+        import torch
+        return torch.cuda.device_count() > 0
+    except Exception:  # pragma: no cover
+        return False
+
+
+# a fake device pointer must never reach a launch on a real device
+pytestmark = pytest.mark.skipif(_gpu_present(), reason="fake device pointers: host-only checks")
+
+A, B, C = 0x100000, 0x200000, 0x300000
+
+
+@pytest.mark.parametrize("t", [1e-45, 2.0 ** -127, 1.17e-38, -1.0])
+def test_temperatures_without_a_finite_reciprocal(t):
+    """1 / T, and log2(e) / T, have to be numbers: NaN came out for T below
+    4.3e-39. Subnormal temperatures are refused."""
+    calls = [
+        lambda: N.lib.kq_top_logits(A, N.KQ_F32, 4, 100, 100, 5, t, B, C, None, None),
+        lambda: N.lib.kq_distill_loss(A, N.KQ_F32, 4, 100, 100, B, C, None, 5, t, None, B, None, None),
+        lambda: N.lib.kq_distill_grad(A, N.KQ_F32, 4, 100, 100, B, C, None, 5, t, B, B, C, 100, None),
+        lambda: N.lib.kq_distill_loss_grad(A, N.KQ_F32, 4, 100, 100, B, C, None, 5, t, None, B, None, C, 100, None),
+    ]
+    for call in calls:
+        assert call() == N.KQ_ERR_ARG
+        assert "temperature" in N.lib.kq_last_error().decode()
+
+
+def test_the_smallest_temperature_is_taken():
+    """(no rows: nothing is launched)"""
+    assert N.lib.kq_top_logits(None, N.KQ_F32, 0, 100, 100, 5, 2.0 ** -126, None, None, None, None) == N.KQ_OK
