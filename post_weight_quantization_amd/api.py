@@ -513,6 +513,11 @@ def kq_pack_i8(codes, zero, packed=None, zero_out=None, stream=None):
     return packed, zero_out
 
 
+def _check_out_dtype(y, dtype):
+    if y is None and dtype not in _DT:
+        raise ValueError(f"dtype: expected torch.bfloat16 or torch.float32, got {dtype}")
+
+
 def _product_out(y, n, d_out, dtype, dev, stream):
     if y is None:
         y = _empty((n, d_out), dtype, dev, stream)
@@ -528,6 +533,7 @@ def kq_matmul_i8(a, a_scale, w, w_scale, d_in: int, a_sum=None, w_zero=None, bia
     """y (n x d_out) = s_t w_o (sum_k a_tk (q_ok - z_o)) + b_o from tokens
     already quantized by kq_quantize_rows. dtype: of y where y is not given."""
     n, d_out = a.shape[0], w.shape[0]
+    _check_out_dtype(y, dtype)
     dev = a.device
     _on_device(dev, a_scale, w, w_scale, a_sum, w_zero, bias, y, ws)
     pa, pw = _codes(a, n, d_in, "a"), _codes(w, d_out, d_in, "w")
@@ -551,11 +557,13 @@ def kq_linear_i8(x, w, w_scale, w_zero=None, bias=None, clip: float = 1.0, y=Non
     given (default: that of x)."""
     n, d_in, ldx = _rows(x, "x")
     d_out = w.shape[0]
+    dtype = dtype or x.dtype
+    _check_out_dtype(y, dtype)
     dev = x.device
     _on_device(dev, w, w_scale, w_zero, bias, y, ws)
     pw = _codes(w, d_out, d_in, "w")
     f32 = torch.float32
-    y, ldy = _product_out(y, n, d_out, dtype or x.dtype, dev, stream)
+    y, ldy = _product_out(y, n, d_out, dtype, dev, stream)
     if ws is None:
         need = _need(N.KQ_OP_LINEAR_I8, d_out, d_in, n)
         ws = _empty((need,), torch.uint8, dev, stream) if need else None

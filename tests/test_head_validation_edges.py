@@ -37,3 +37,20 @@ def test_temperatures_without_a_finite_reciprocal(t):
 def test_the_smallest_temperature_is_taken():
     """(no rows: nothing is launched)"""
     assert N.lib.kq_top_logits(None, N.KQ_F32, 0, 100, 100, 5, 2.0 ** -126, None, None, None, None) == N.KQ_OK
+
+
+def test_output_types_the_product_does_not_write():
+    import torch
+
+    from post_weight_quantization_amd import api
+
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt)
+    w = z(3, 128, dt=torch.int8)
+    for dtype in (torch.float16, torch.float64, torch.int8):
+        with pytest.raises(ValueError, match="^dtype: expected"):
+            api.kq_linear_i8(z(4, 8), w, z(3), dtype=dtype)
+        with pytest.raises(ValueError, match="^dtype: expected"):
+            api.kq_matmul_i8(z(4, 128, dt=torch.int8), z(4), w, z(3), 8, dtype=dtype)
+    # a matrix of the caller's decides for itself
+    with pytest.raises(ValueError, match="GPU"):
+        api.kq_linear_i8(z(4, 8), w, z(3), y=z(4, 3), dtype=torch.float16)
