@@ -60,12 +60,20 @@ __device__ inline float masked(float v, uint32_t keep) { return __uint_as_float(
 struct Pair {
   float off, on;
 };
-struct PairMax {
-  __device__ Pair operator()(Pair a, Pair b) const { return {Max()(a.off, b.off), Max()(a.on, b.on)}; }
-};
-struct PairSum {
-  __device__ Pair operator()(Pair a, Pair b) const { return {a.off + b.off, a.on + b.on}; }
-};
+
+// f over the workgroup's pairs (see block_reduce); the second halves of waves
+// that `lists` does not name are `none`
+template <int TPB, class F>
+__device__ inline Pair block_reduce_pairs(Pair v, bool lists, float none, Pair* part, F f) {
+  v.off = wave_reduce(v.off, f);
+  v.on = lists ? wave_reduce(v.on, f) : none;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  Pair r = part[0];
+#pragma unroll
+  for (int w = 1; w < TPB / 64; ++w) r = {f(r.off, part[w].off), f(r.on, part[w].on)};
+  return r;
+}
 
 struct DistillArgs {
   int64_t n, ld, ldg;
@@ -84,8 +92,9 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
   constexpr int CH = V::CH, TPB = V::TPB;
   extern __shared__ uint32_t bits[];  // a bit per column: on the list
   __shared__ double dpart[2][TPB / 64];
-  __shared__ float fpart[2][TPB / 64];
+  __shared__ float fpart[4][TPB / 64];
   __shared__ Pair pair[2][TPB / 64];
+  __shared__ int twice;  // a column is on the list more than once (known with the bucket)
   __shared__ __align__(16) int idx_at[K_MAX];
   __shared__ __align__(16) float p_at[K_MAX];
   static_assert(K_MAX <= TPB, "one thread per entry of the list");
@@ -96,6 +105,7 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
   if (bucket)
     for (int j = t; j < int(cdiv(d.vocab, 32)); j += TPB) bits[j] = 0;
   for (int j = t; j < K_MAX; j += TPB) idx_at[j] = -1, p_at[j] = 0.f;
+  if (t == 0) twice = bucket ? 0 : 1;
   __syncthreads();
   Row<T, V> r;
   r.load(logits + int64_t(blockIdx.x) * d.ld, full, d.vocab);
@@ -120,7 +130,7 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
       if (idx >= 0) {
         at_idx = to_f32(lr[idx]);
         tv = d.t_values[row * d.k + t];
-        if (bucket) atomicOr(&bits[idx >> 5], 1u << (idx & 31));
+        if (bucket && atomicOr(&bits[idx >> 5], 1u << (idx & 31)) >> (idx & 31) & 1) twice = 1;
       }
     }
     double mass = 1.0, rest = 0.0;
@@ -143,7 +153,7 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
       if (total == 0.f) mass = 0.0;
     }
     const float p = idx >= 0 ? __builtin_amdgcn_exp2f(log_p) : 0.f;
-    if (t < d.k) p_at[t] = p;
+    if (GRAD && t < d.k) p_at[t] = p;
     if (bucket) {
       mass = uniform(block_reduce<TPB>(double(p), dpart[0], Sum()));
       rest = 1.0 - mass;
@@ -152,10 +162,13 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
     } else {
       __syncthreads();
     }
-    // entries of one column: the first counts and writes for all
-    float p_col = 0.f;
+    // Entries of one column: the first counts and writes for all. All are compared
+    // with all only where the bits have met such a column (loss of 20000 x 4000
+    // with lists of 256: 74 us, 370 where every row is).
+    float p_col = p;
     bool first = (GRAD || bucket) && idx >= 0;
-    if (first) {
+    if (first && twice) {
+      p_col = 0.f;
       for (int l = 0; l < d.k; l += 4) {
         const int4 other = *reinterpret_cast<const int4*>(idx_at + l);
         if (GRAD) {
@@ -213,30 +226,36 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
       o.raise(tail, c, rescale);
       off += __builtin_amdgcn_exp2f((tail - o.m) * c);
       if (!GRAD && more) r.load_tail(nr, full, d.vocab);
-      const float listed = bucket && first ? at_idx : -__builtin_inff();
-      Pair tops = block_reduce<TPB>(Pair{top, max3(listed, LOWEST, LOWEST)}, pair[0], PairMax());
-      tops = {uniform(tops.off), uniform(tops.on)};
-      rescale(__builtin_amdgcn_exp2f((o.m - tops.off) * c));
-      const float on = __builtin_amdgcn_exp2f((listed - tops.on) * c);
-      Pair sums = block_reduce<TPB>(Pair{off, on}, pair[1], PairSum());
-      sums = {uniform(sums.off), uniform(sums.on)};
-      // (LOWEST is the maximum of no logit, and its sum 0)
-      m = Max()(tops.off, tops.on);
-      off = sums.off;
-      const float scaled_off = off * __builtin_amdgcn_exp2f((tops.off - m) * c);
-      total = scaled_off + sums.on * __builtin_amdgcn_exp2f((tops.on - m) * c);
+      float top_off, scaled_off;  // (LOWEST is the maximum of no logit, and its sum 0)
+      if (bucket) {
+        const float listed = first ? at_idx : -__builtin_inff();
+        const bool lists = (t & ~63) < d.k;  // whether the wave has entries
+        const Pair tops =
+            block_reduce_pairs<TPB>(Pair{top, max3(listed, LOWEST, LOWEST)}, lists, LOWEST, pair[0], Max());
+        rescale(__builtin_amdgcn_exp2f((o.m - tops.off) * c));
+        const float on = __builtin_amdgcn_exp2f((listed - tops.on) * c);
+        const Pair sums = block_reduce_pairs<TPB>(Pair{off, on}, lists, 0.f, pair[1], Sum());
+        top_off = uniform(tops.off), off = uniform(sums.off);
+        m = uniform(Max()(tops.off, tops.on));
+        scaled_off = off * __builtin_amdgcn_exp2f((top_off - m) * c);
+        total = uniform(scaled_off + sums.on * __builtin_amdgcn_exp2f((tops.on - m) * c));
+      } else {
+        m = top_off = uniform(block_reduce<TPB>(top, fpart[2], Max()));
+        rescale(__builtin_amdgcn_exp2f((o.m - m) * c));
+        off = total = scaled_off = uniform(block_reduce<TPB>(off, fpart[3], Sum()));
+      }
       if (total == 0.f) m = 0.f;
       // to base 2; a row without a finite logit has q = 0 and log q = -inf
       const float log_total = total == 0.f ? 0.f : __builtin_amdgcn_logf(total);
-      const double log_q_r = off == 0.f ? -double(__builtin_inff())
-                                        : (double(tops.off) - double(m)) * double(c) +
-                                              double(__builtin_amdgcn_logf(off)) - double(log_total);
-      q_r = scaled_off / total;
-      ref = tops.off, log_ref = 0.f;
+      if (GRAD) q_r = scaled_off / total;
+      ref = top_off, log_ref = 0.f;
       double term = 0.0;
       if (p > 0.f) term = double(p) * ((double(log_p) - double(at_idx - m) * double(c)) + double(log_total));
       term = block_reduce<TPB>(term, dpart[1], Sum());
       if (t == 0) {
+        const double log_q_r = off == 0.f ? -double(__builtin_inff())
+                                          : (double(top_off) - double(m)) * double(c) +
+                                                double(__builtin_amdgcn_logf(off)) - double(log_total);
         if (rest > 0.0) term += rest * (double(__builtin_amdgcn_logf(float(rest))) - log_q_r);
         d.loss[row] = masked(float(double(w) * d.temperature * d.temperature * LN2 * term), keep);
         if (d.stats) {
@@ -288,6 +307,7 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void distill_kernel(const T* logi
       __syncthreads();
     }
     if (bucket && idx >= 0) bits[idx >> 5] = 0;
+    if (bucket && t == 0) twice = 0;
     __syncthreads();
   }
 }
@@ -320,12 +340,14 @@ kq_status distill_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab,
     const std::false_type no;
     // What is chosen goes by the row's length alone, so that a row's sums, and
     // their rounding, are the same in whatever company.
-    // One pass, nothing to hold: loss of 20000 x 4000 bf16 66 us with 256 threads
-    // and room for 8 waves, 74 with 6; of 4096 x 32000 54 with 256 and 6, 59 with
+    // One pass, nothing to hold: loss of 20000 x 4000 bf16 without a bucket 57 us
+    // with 256 threads and room for 8 waves, which spills 12 bytes a lane, 58.5
+    // with 7, 67 with 6; with a bucket and lists of 256 74 with 8 and 72 with 7, of
+    // 8192 x 8000 and 200 46.6 and 43.2; of 4096 x 32000 54 with 256 and 6, 59 with
     // 8, 66 with 512 threads; of 1 x 128256 24 with 256, 16 with 512, and of 4096
     // of them 162 and 172.
     if (!grad) {
-      if (chunks <= 1024) return go(Variant<0, 256, 8>(), yes, no);
+      if (chunks <= 1024) return t_lse ? go(Variant<0, 256, 7>(), yes, no) : go(Variant<0, 256, 8>(), yes, no);
       if (chunks <= 4096) return go(Variant<0, 256, 6>(), yes, no);
       return go(Variant<0, 512, 6>(), yes, no);
     }
