@@ -28,7 +28,9 @@
 // The log-sum-exp is that of the quotients l / T as the distillation rounds
 // them: of a list with nearly all of the mass, what it leaves is a difference of
 // numbers that both round alike (T = 0.7, l / T near 60: within 2e-6, else up to
-// 4e-6). Only listed logits are corrected for it; the others' mass is then small.
+// 4e-6). The candidates are corrected for it, to first order, each by its share
+// times its quotient's rounding; where a list has nearly all of the mass, the
+// others have little.
 //
 // 64 of 4096 x 128256 bf16 take 206 us, 5.1 TB/s; vector instructions bound it:
 // they keep the SIMDs busy 83 % of the time, half of that an exponential per
@@ -76,6 +78,15 @@ __device__ inline float quotient(float v, float inv_t) {
 }
 __device__ inline float quotient_error(float v, float inv_t) { return -fmaf(v, inv_t, -quotient(v, inv_t)); }
 
+// the sum of a row's exponentials, and of candidates' exponentials times what
+// the rounding of their quotients adds
+struct Sums {
+  float all, moved;
+};
+struct Join {
+  __device__ Sums operator()(Sums a, Sums b) const { return {a.all + b.all, a.moved + b.moved}; }
+};
+
 template <int NW>
 struct TopLds {
   __align__(16) uint64_t list[LIST + 2];
@@ -85,8 +96,9 @@ struct TopLds {
   __align__(16) uint16_t group[GROUPS];
   int pivots[2][16];
   float part[NW];
-  float shift[K_MAX];
-  float sums[NW];  // apart from `part`, which a wave may still read when another is done with the row
+  // apart from `part`, which a wave may still read when another is done with the row
+  float sum[NW];
+  Sums sums[NW];
   int ipart[2][NW];
   int count, overflow;
 };
@@ -154,7 +166,8 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int full = vocab / E<T>;
   const float c = inv_t * 1.44269504088896340736f;
-  const bool inexact = lse && (__float_as_uint(inv_t) & 0x7fffffu) != 0;
+  // whether quotients round, and someone asks for their sum
+  const bool rounds = lse && (__float_as_uint(inv_t) & 0x7fffffu) != 0;
   Row<T, V> r;
   r.load(logits + int64_t(blockIdx.x) * ld, full, vocab);
   for (int row = blockIdx.x; row < n; row += gridDim.x) {
@@ -261,9 +274,14 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
       if constexpr (CH > 0) r.load_chunk(i, nr, ahead);
     });
     // the elements of the wave's chunks, and the tail, at or above tau
+    float moved = 0.f;
     auto append = [&](bool take, float v, int j) {
       const uint64_t takes = __ballot(take);
       if (!takes) return;
+      if (rounds) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(v, scale, -ref));
+        if (take && e > 0.f) moved += e * quotient_error(v, inv_t);
+      }
       int base = 0;
       if (lane == 0) base = atomicAdd(&s.count, __popcll(takes));
       const int at = __builtin_amdgcn_readfirstlane(base) + lanes_below(takes);
@@ -283,16 +301,19 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
       const float v = __uint_as_float(E<T> == 4 ? word : e & 1 ? word & 0xffff0000u : word << 16);
       append(i < items && v >= tau, v, s.chunk_no[w][at] * E<T> + e);
     }
-    sum = block_reduce<TPB>(sum, s.sums, Sum());
-    // the log-sum-exp, where no quotient rounds (1 / T a power of 2) or it is not a
-    // finite number (no finite logit: the sum is 0; NaN: the row's largest, found
-    // below, is the answer; a quotient past fp32 is the answer), else less what the
-    // listed quotients' rounding moves it by
-    const bool rounds = inexact && sum > 0.f && fabsf(m * inv_t) < __builtin_inff();
-    float rel = 0.f;  // of the row against its largest
-    if (lse && w == 0 && sum == sum) {
-      rel = logf(sum) + fmaf(-m, scale, ref) * 0.69314718055994530942f;
-      if (lane == 0 && !rounds) lse[row] = sum == 0.f ? -__builtin_inff() : m * inv_t + rel;
+    if (rounds) {
+      const Sums sums = block_reduce<TPB>(Sums{sum, moved}, s.sums, Join());
+      sum = sums.all, moved = sums.moved;
+    } else {
+      sum = block_reduce<TPB>(sum, s.sum, Sum());
+    }
+    // (NaN: the row's largest, found below, is the answer; no finite logit: the sum
+    // is 0; a quotient past fp32 is the answer)
+    if (lse && t == 0 && sum == sum) {
+      const float top = quotient(m, inv_t);
+      const float rel = logf(sum) + fmaf(-m, scale, ref) * 0.69314718055994530942f;
+      const float by = moved / sum - quotient_error(m, inv_t);
+      lse[row] = sum == 0.f ? -__builtin_inff() : isinf(top) ? top : top + (rel + by);
     }
     int count = s.count;
     if (s.overflow || count > LIST || sum != sum) {
@@ -330,11 +351,23 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
     for (int i = t & (width - 1); i < count; i += width) {
       const uint64_t mine = s.list[i];
       uint32_t before = 0;
-#pragma unroll 4
-      for (int j = 2 * (t / width); j < count; j += 2 * (TPB / width)) {
-        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(s.list + j);
-        before += (two.x > mine) + (two.y > mine);
+      const int step = 2 * (TPB / width);
+      auto count_above = [&](const ulonglong2& two) { before += (two.x > mine) + (two.y > mine); };
+      auto pair_at = [&](int j) { return *reinterpret_cast<const ulonglong2*>(s.list + j); };
+      int j = 2 * (t / width);
+      // four pairs on their way before the first is compared (in turn, 256 of 4096
+      // x 32000 took 133 us for 119)
+#pragma unroll 1
+      for (; j + 3 * step < count; j += 4 * step) {
+        ulonglong2 pairs[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pairs[u] = pair_at(j + u * step);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) count_above(pairs[u]);
       }
+#pragma unroll 1
+      for (; j < count; j += step) count_above(pair_at(j));
       if (before) atomicAdd(&s.rank[i], before);
     }
     __syncthreads();
@@ -345,21 +378,10 @@ __global__ __launch_bounds__(V::TPB, V::WAVES) void top_logits_kernel(const T* _
         const float v = value_of(uint32_t(s.list[i] >> 32));
         values[int64_t(row) * k + at] = v;
         if (at == 0 && lse && sum != sum) lse[row] = v;  // +inf, or NaN, which is above it
-        if (rounds) {  // to first order: the entry's share times the rounding
-          const float share = __builtin_amdgcn_exp2f(fmaf(v, scale, -ref)) / sum;
-          s.shift[at] = share > 0.f ? share * quotient_error(v, inv_t) : 0.f;
-        }
         index[int64_t(row) * k + at] = int32_t(~uint32_t(s.list[i]));
       }
     }
     __syncthreads();
-    // (the first wave; s.shift is written again several barriers later)
-    if (rounds && w == 0) {
-      float moved = 0.f;
-      for (int i = lane; i < k; i += 64) moved += s.shift[i];
-      moved = wave_reduce(moved, Sum()) - quotient_error(m, inv_t);
-      if (lane == 0) lse[row] = quotient(m, inv_t) + (rel + moved);
-    }
   }
 }
 
