@@ -884,11 +884,22 @@ I8Plan i8_plan(int64_t n, int64_t m, int64_t d) {
 }
 
 // Whether the tokens are rounded within the product: it takes the place of a
-// launch and a pass through memory (1 token, 4096 -> 4096: 10.7 us, so 7.7; 4
-// tokens: 11.0, 9.4; 8 tokens of 1000: 6.6, 6.8), but every workgroup does it
-// (4 tokens, 2048 -> 28672: 20 us, so 40; 16 tokens of 1024: 7.1, 8.1).
+// launch (the host's time for it, 2.5 us, too) and a pass through memory, but
+// every workgroup does it, 256 at a time, 16 channels each. us of the kernels
+// rounded within, and apart:
+//   1 token   4096 ->  4096   6.3,  9.9    4096 -> 12288  14.4, 16.7
+//   1 token  16384 ->  6144  29.4, 32.3   16384 -> 12288  45.7, 42.3
+//   2 tokens  4096 ->  8192  11.4, 13.1    4096 -> 12288  15.4, 16.8
+//   2 tokens  8192 ->  6144  18.0, 18.2    8192 -> 12288  26.9, 24.2
+//   4 tokens  4096 ->  4096   8.2, 10.4    4096 ->  5120  13.1, 12.8
+//   8 tokens  2048 ->  4096   7.0,  7.4    2048 ->  5120  11.7,  8.8
+//   8 tokens  1024 ->  8192   8.8,  7.4 (with the host's time 8.7, 10.7)
+//   8 tokens  1024 -> 12288  13.0,  8.8
 bool i8_fused(int64_t n, int64_t m, int64_t d) {
-  return n <= 8 && m <= 12288 && (16 / fused_waves(n)) * d <= 16384;
+  if (n > 8 || (16 / fused_waves(n)) * d > 16384) return false;  // its registers
+  if (m <= 4096) return true;
+  if (m <= 8192) return n * d < 16384 || (n <= 2 && m <= 6144);
+  return m <= 12288 && d > 2048 && n * d <= 8192;
 }
 
 }  // namespace
