@@ -17,9 +17,9 @@
 // are written again after a barrier. (Without a bucket every column counts as
 // off the list, and the factor is w T P / sum e.) For loss and gradient in one call rows of
 // up to 128 KB stay in registers between the passes, so the logits are read
-// once and the gradient written once: memory bounds it (4096 x 32000 bf16: 110
+// once and the gradient written once: memory bounds it (4096 x 32000 bf16: 109
 // us, 4.8 TB/s; copying runs at 5.2). Longer rows are read twice (8192 x 128256
-// bf16: 916 us, 4.6 TB/s of one read and one write, the second read beside
+// bf16: 911 us, 4.6 TB/s of one read and one write, the second read beside
 // them). The teacher's side is computed by the first K threads while the row
 // is on its way.
 //
@@ -359,10 +359,10 @@ kq_status distill_run(const void* logits, kq_dtype dt, int64_t n, int64_t vocab,
       return go(Variant<0, 1024, 8>(), no, yes);
     }
     // Loss and gradient: two passes. Rows of up to 128 KB are held in
-    // registers (4096 x 32000 bf16: 117 us, read twice 128; 4096 x 65536: 224,
-    // 232); of longer ones a CU holds too few at once to keep the memory
-    // busy, and the second pass finds them in the cache beside it (4096 x
-    // 128256: 453 us, in registers 531 to 599).
+    // registers (4096 x 32000 bf16, the same rows each time: 115 us, read twice
+    // 121; 4096 x 65536: 215, 229); of longer ones a CU holds too few at once to
+    // keep the memory busy, and the second pass finds them in the cache beside it
+    // (4096 x 128256: 451 us, in registers 493).
     if (chunks <= 512) return go(Variant<2, 256, 6>(), yes, yes);
     if (chunks <= 1024) return go(Variant<4, 256, 6>(), yes, yes);
     if (chunks <= 2048) return go(Variant<8, 256, 5>(), yes, yes);

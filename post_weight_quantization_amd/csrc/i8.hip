@@ -172,7 +172,9 @@ __global__ __launch_bounds__(TPB) void quantize_rows_kernel(const T* __restrict_
   }
 }
 
-// codes of the sweep (0 .. 255) as signed bytes q - 128, rows padded with 0
+// codes of the sweep (0 .. 255) as signed bytes q - 128, rows padded with 0. Once
+// for a layer: a byte a thread and step, 1.7 TB/s (8192 x 28672: 270 us, a copy
+// 90).
 __global__ __launch_bounds__(256) void pack_i8_kernel(const uint8_t* __restrict__ codes,
                                                       const float* __restrict__ zero, int64_t d,
                                                       int64_t row_bytes, int8_t* __restrict__ packed,
@@ -581,7 +583,7 @@ __global__ __launch_bounds__(64 * SW) void stream_i8_kernel(const int8_t* __rest
 // The same where many channels meet several tokens. There every 16 channels
 // read all tokens' codes once more, and from the caches that takes as long as
 // the channels' own bytes do from memory (28672 -> 8192: 43 us with 1 token, 58
-// with 12, and 44 with 12 whose loads all take one line). So a workgroup keeps
+// with 12). So a workgroup keeps
 // its share of the tokens in registers, U lines a wave, U * SW at most, and
 // goes from 16 channels to the next, which are loaded while these are
 // multiplied: 12 tokens 48 us, with the launch that joins the shares; without

@@ -32,11 +32,12 @@
 // times its quotient's rounding; where a list has nearly all of the mass, the
 // others have little.
 //
-// 64 of 4096 x 128256 bf16 take 206 us, 5.1 TB/s; vector instructions bound it:
+// 64 of 4096 x 128256 bf16 take 207 us, 5.1 TB/s; vector instructions bound it:
 // they keep the SIMDs busy 83 % of the time, half of that an exponential per
 // element, at a quarter of the rate of the others. One row alone takes its CU 13
-// us, spent the same way; it is not shared among CUs, whose sums would join in an
-// order that many rows do not have.
+// us, spent the same way; it is not shared among CUs (which would have to join
+// its waves' sums in their order here, for a row to be the same bits in whatever
+// company).
 #include <type_traits>
 
 #include "logits_rows.h"
@@ -405,7 +406,7 @@ kq_status top_logits_run(const void* logits, kq_dtype dt, int64_t n, int64_t voc
     // a thread (4096 x 32000 bf16: 64 us with 256 threads, 98 with 512; 512 x
     // 50001 fp32, lists of 200: 31.7 us with 16 chunks of 1024 threads, 34.1
     // with 32 of 512), and the largest rows that fit too (4096 x 128256 bf16:
-    // 208 us, read twice 290). The number of rows has no say, so that a row's sum,
+    // 207 us, read twice 290). The number of rows has no say, so that a row's sum,
     // and its rounding, is the same in whatever company.
     if (chunks <= 1024) return go(Variant<4, 256, 6>());
     if (chunks <= 2048) return go(Variant<8, 256, 5>());

@@ -38,7 +38,10 @@ def _without_gradient(name, t):
 
 @dataclass
 class I8Linear:
-    """y = x W^T + b in 8-bit integers (see kq_linear_i8)."""
+    """y = x W^T + b in 8-bit integers (see kq_linear_i8), in the basis that the
+    codes were made in: codes of a layer that ``layer.prepare_layer`` turned
+    (incoherence processing) take tokens turned the same way, and give outputs
+    in its turned basis; nothing is transformed here."""
 
     codes: torch.Tensor          # int8, d_out x kq_i8_row_bytes(d_in)
     scale: torch.Tensor          # fp32, d_out
