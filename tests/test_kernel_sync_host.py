@@ -31,7 +31,7 @@ def test_a_wait_state_between_m0_and_the_load_into_lds():
         for text in re.findall(r'asm volatile\(\s*"((?:[^"\\]|\\.)*)"', _source(name)):
             ops = [o.strip() for o in text.replace("\\t", "").split("\\n")]
             for at, op in enumerate(ops):
-                if op.startswith("s_mov_b32 m0"):
+                if re.match(r"s_\w+ m0\b", op):
                     seen += 1
                     assert "lds" not in ops[at + 1], (name, text)
     assert seen >= 3
